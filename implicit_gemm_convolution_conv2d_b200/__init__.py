@@ -20,7 +20,8 @@ __all__ = ["conv_fwd", "conv_fwd_host", "out_dims", "plan", "conv_transpose", "t
            "CONV_F32", "CONV_F16", "CONV_BF16", "VARIANT_AUTO", "VARIANT_SIMT", "VARIANT_TC_TMA",
            "VARIANT_TC_GATHER", "VARIANT_TC_TMA_PAIR", "VARIANT_TC_HALO", "VARIANT_TC_HALO_PAIR",
            "VARIANT_TC_TMA_T", "VARIANT_TC_HALO_T", "VARIANT_TC_HALO_T_PAIR", "VARIANT_TC_PHASE", "VARIANT_DEPTHWISE", "VARIANT_DEPTHWISE_DIRECT",
-           "VARIANT_TC_TMA_PHASES", "VARIANT_TC_STAGED", "ConvError"]
+           "VARIANT_TC_TMA_PHASES", "VARIANT_TC_STAGED", "ConvError", "conv_causal", "conv_causal_grad",
+           "conv_causal_step", "gated_scan", "gated_scan_grad", "gated_scan_step", "Act8", "act8_pack", "act8_unpack"]
 
 CONV_F32, CONV_F16, CONV_BF16 = 0, 1, 2
 VARIANT_AUTO, VARIANT_SIMT, VARIANT_TC_TMA, VARIANT_TC_GATHER, VARIANT_TC_TMA_PAIR = -1, 0, 1, 2, 3
@@ -233,12 +234,21 @@ def conv_wgrad(x, dy, kernel_size, stride=1, padding=0, dilation=1, groups=1, *,
                workspace=None, stream=None):
     """Weight gradient of conv_fwd: dw[o, k, c] = sum over output pixels of dy * x.
 
-    x: [N, (D,) H, W, C]; dy: [N, (Do,) Ho, Wo, O]; kernel_size: (kD,) kH, kW.
-    Returns dw [O, (kD,) kH, kW, C/groups] in x's dtype.  The call needs an
+    x: [N, (D,) H, W, C], or its 8-bit checkpoint (Act8), which is unpacked
+    into a temporary of dy's type; dy: [N, (Do,) Ho, Wo, O]; kernel_size: (kD,)
+    kH, kW.  Returns dw [O, (kD,) kH, kW, C/groups] in x's dtype.  The call needs an
     fp32 workspace of wgrad_workspace_size bytes; one is allocated with torch
     when `workspace` is None.
     """
     import torch
+    from .seq import Act8, act8_unpack
+    if isinstance(x, Act8):
+        if not (x.q.is_cuda and dy.is_cuda):
+            raise ValueError("conv_wgrad runs on CUDA tensors only")
+        st = stream if stream is not None else torch.cuda.current_stream(dy.device)
+        with torch.cuda.stream(st):
+            return conv_wgrad(act8_unpack(x), dy, kernel_size, stride, padding, dilation, groups,
+                              padding_hi=padding_hi, out=out, workspace=workspace)
     if not (x.is_cuda and dy.is_cuda):
         raise ValueError("conv_wgrad runs on CUDA tensors only")
     if x.dtype != dy.dtype:
@@ -420,3 +430,13 @@ def last_status(stream=None) -> int:
     import torch
     st = stream if stream is not None else torch.cuda.current_stream()
     return int(lib().conv_last_status(st.cuda_stream))
+
+
+def __getattr__(name):
+    """The sequence operators (seq.py) are loaded, with torch, at their first use."""
+    if name in ("seq", "conv_causal", "conv_causal_grad", "conv_causal_step", "gated_scan", "gated_scan_grad",
+                "gated_scan_step", "Act8", "act8_pack", "act8_unpack"):
+        import importlib
+        mod = importlib.import_module(".seq", __name__)
+        return mod if name == "seq" else getattr(mod, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

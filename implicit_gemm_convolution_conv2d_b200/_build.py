@@ -8,15 +8,16 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libconvfwd.so")
-SOURCES = [os.path.join(CSRC, "conv_fwd.cu"), os.path.join(CSRC, "conv_wgrad.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("conv_fwd.cu", "conv_wgrad.cu", "conv_causal.cu", "gated_scan.cu", "act8.cu")]
 DEPS = SOURCES + sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")) + [
-    os.path.join(os.path.dirname(HERE), "include", "conv_fwd.h")]
+    os.path.join(os.path.dirname(HERE), "include", f) for f in ("conv_fwd.h", "conv_seq.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-shared",
     "--expt-relaxed-constexpr",
+    "--threads", "0",  # the sources side by side
 ]
 
 
