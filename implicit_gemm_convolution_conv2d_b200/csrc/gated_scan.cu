@@ -23,16 +23,69 @@ int take_input(ScanIn& in, Span* s, const void* p, const unsigned char* scale, l
   return CONV_OK;
 }
 
-template <typename T>
-cudaError_t launch_forward(const ScanArgs& a, cudaStream_t st) {
-  const dim3 grid((a.C + kScanThreads - 1) / kScanThreads, a.N);
-  return launch_pdl(gated_scan_kernel<T>, grid, dim3(kScanThreads), 0, st, 1, a);
+// CTAs of a cluster, `tokens` each: enough that the grid has four CTAs for each
+// SM of a 148-SM B200 (a fixed number: the order of ddecay's sum must not depend
+// on the device), but no more than the tokens fill.
+int cluster_of(int N, long long L, int C, bool packed, int tokens) {
+  const long long chains = (packed ? 1LL : N) * ((C + 63) / 64);
+  const long long turns = (L + tokens - 1) / tokens;
+  int s = 1;
+  while (s < kScanMaxCluster && s < turns && chains * s < 4 * 148) s *= 2;
+  return s;
+}
+
+bool rows_take16(const ScanIn& in, bool packed, int esize) {
+  return rows_aligned(in.p, packed ? 0 : in.batch, in.token, in.scale ? 1 : esize, 16);
+}
+
+bool rows_take(const ScanIn& in, bool packed, int esize, int V) {
+  const int es = in.scale ? 1 : esize;
+  return rows_aligned(in.p, packed ? 0 : in.batch, in.token, es, static_cast<size_t>(es) * V);
+}
+
+template <typename T, bool PACKED, bool ALIGNED>
+cudaError_t forward_as(const ScanArgs& a, cudaStream_t st) {
+  const int s = cluster_of(a.N, a.L, a.C, PACKED, kScanWarps * kForwardSteps);
+  const dim3 grid((a.C + 63) / 64 * s, PACKED ? 1 : a.N);
+  auto* k = gated_scan_kernel<T, PACKED, ALIGNED>;
+  const size_t smem = sizeof(ForwardShared<T>);
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  return e != cudaSuccess ? e : launch_pdl(k, grid, dim3(kScanThreads), smem, st, s, a);
 }
 
 template <typename T>
-cudaError_t launch_grad(const ScanArgs& a, cudaStream_t st) {
-  const dim3 grid((a.C + kScanThreads - 1) / kScanThreads, a.N);
-  return launch_pdl(gated_scan_grad_kernel<T>, grid, dim3(kScanThreads), 0, st, 1, a);
+cudaError_t launch_forward(const ScanArgs& a, cudaStream_t st) {
+  const bool p = a.packed, aligned = a.C % (16 / static_cast<int>(sizeof(T))) == 0 && rows_take16(a.x, p, sizeof(T)) &&
+                                     rows_take16(a.r, p, sizeof(T)) && rows_take16(a.i, p, sizeof(T)) &&
+                                     aligned_to(a.y, 2 * sizeof(T));
+  if (aligned) return p ? forward_as<T, true, true>(a, st) : forward_as<T, false, true>(a, st);
+  return p ? forward_as<T, true, false>(a, st) : forward_as<T, false, false>(a, st);
+}
+
+template <typename T, int V, bool PACKED, bool Q8>
+cudaError_t grad_as(const ScanArgs& a, int& parts, cudaStream_t st) {
+  const int s = cluster_of(a.N, a.L, a.C, PACKED, GATED_SCAN_STATE_EVERY);
+  const dim3 grid((a.C + 32 * V - 1) / (32 * V) * s, PACKED ? 1 : a.N);
+  parts = s * static_cast<int>(grid.y);
+  return launch_pdl(gated_scan_grad_kernel<T, V, PACKED, Q8>, grid, dim3(kScanThreads), 0, st, s, a);
+}
+
+template <typename T, int V>
+cudaError_t grad_by(const ScanArgs& a, int& parts, cudaStream_t st) {
+  if (a.x.scale || a.r.scale || a.i.scale)
+    return a.packed ? grad_as<T, V, true, true>(a, parts, st) : grad_as<T, V, false, true>(a, parts, st);
+  return a.packed ? grad_as<T, V, true, false>(a, parts, st) : grad_as<T, V, false, false>(a, parts, st);
+}
+
+// `parts`: the partial sums of ddecay.
+template <typename T>
+cudaError_t launch_grad(const ScanArgs& a, int& parts, cudaStream_t st) {
+  constexpr int kV = 2;
+  const bool p = a.packed;
+  bool vec = a.C % kV == 0;
+  for (const ScanIn* in : {&a.x, &a.r, &a.i, &a.dy}) vec = vec && rows_take(*in, p, sizeof(T), kV);
+  for (const void* out : {a.dx, a.dr, a.di}) vec = vec && aligned_to(out, sizeof(T) * kV);
+  return vec ? grad_by<T, kV>(a, parts, st) : grad_by<T, 1>(a, parts, st);
 }
 
 template <typename T>
@@ -85,6 +138,7 @@ int gated_scan(const void* x, const void* r, const void* i, const float* decay, 
     return CONV_OK;
   }
   a.decay = decay;
+  a.consts = gate_consts();
   a.h0 = h0;
   a.cu = cu;
   a.y = y;
@@ -103,7 +157,7 @@ int gated_scan(const void* x, const void* r, const void* i, const float* decay, 
 
 int gated_scan_grad_workspace_size(int N, long long L, int C, int packed, unsigned long long* bytes) {
   if (!seq_sizes_ok(N, L, C, packed != 0) || !bytes) return CONV_EINVAL;
-  *bytes = 4ull * N * C;
+  *bytes = 4ull * (packed ? 1 : N) * kScanMaxCluster * C;  // a row a CTA of a channel
   return CONV_OK;
 }
 
@@ -148,6 +202,7 @@ int gated_scan_grad(const void* x, const unsigned char* x_scale, const void* r, 
   if (any_alias(outs, 6, ins, 13)) return CONV_EALIAS;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   a.decay = decay;
+  a.consts = gate_consts();
   a.states_in = states;
   a.h0 = h0;
   a.cu = cu;
@@ -163,19 +218,20 @@ int gated_scan_grad(const void* x, const unsigned char* x_scale, const void* r, 
   a.C = C;
   a.packed = packed;
   a.fill = fill != 0;
+  int parts = 0;
   if (N == 0) {
     const size_t bytes = static_cast<size_t>(rows) * C * es;
     if (fill && rows > 0)
       for (void* p : {dx, dr, di})
         if (cudaMemsetAsync(p, 0, bytes, st) != cudaSuccess) return CONV_ELAUNCH;
   } else {
-    const cudaError_t e = dtype == CONV_F32   ? launch_grad<float>(a, st)
-                          : dtype == CONV_F16 ? launch_grad<__half>(a, st)
-                                              : launch_grad<__nv_bfloat16>(a, st);
+    const cudaError_t e = dtype == CONV_F32   ? launch_grad<float>(a, parts, st)
+                          : dtype == CONV_F16 ? launch_grad<__half>(a, parts, st)
+                                              : launch_grad<__nv_bfloat16>(a, parts, st);
     if (e != cudaSuccess) return CONV_ELAUNCH;
   }
-  const cudaError_t e = launch_pdl(gated_scan_sum_kernel, dim3((C + kScanThreads - 1) / kScanThreads),
-                                   dim3(kScanThreads), 0, st, 1, static_cast<const float*>(a.part), ddecay, N, C);
+  const cudaError_t e = launch_pdl(gated_scan_sum_kernel, dim3((C + 63) / 64), dim3(64), 0, st, 1,
+                                   static_cast<const float*>(a.part), ddecay, parts, C);
   return e == cudaSuccess ? CONV_OK : CONV_ELAUNCH;
 }
 
@@ -200,7 +256,7 @@ int gated_scan_step(const void* x, const void* r, const void* i, const float* de
   outs[0] = span_of(y, static_cast<long long>(B) * C * es);
   outs[1] = span_of(h, 4LL * slots * C);
   if (any_alias(outs, 2, ins, 8)) return CONV_EALIAS;
-  const ScanStepArgs a = {x, r, i, decay, h, index, y, B, slots, C, fill != 0, x_token, r_token, i_token};
+  const ScanStepArgs a = {x, r, i, decay, h, index, y, B, slots, C, fill != 0, x_token, r_token, i_token, gate_consts()};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == CONV_F32   ? launch_step<float>(a, st)
                         : dtype == CONV_F16 ? launch_step<__half>(a, st)

@@ -16,33 +16,127 @@
 //   dr = -decay dl s (1 - s),  ddecay = -sum s dl,  dh0 = a[0] G[0]
 #pragma once
 
+#include <cmath>
+
+#include "ptx.cuh"
 #include "seq_common.cuh"
 
 namespace convfwd {
 
+// Constants of the gates, as pairs for packed instructions: kernel parameters,
+// so that they are operands of an instruction (an immediate pair is not: it
+// costs two moves each time).
+struct GateConsts {
+  float2 nlog2e, one, nhalf, p3, p4, p5, p6, two, none;
+};
+inline GateConsts gate_consts() {
+  const auto two = [](float v) { return make_float2(v, v); };
+  return GateConsts{two(-kLog2e),        two(1.f),           two(-0.5f), two(1.f / 6.f), two(-1.f / 24.f),
+                    two(1.f / 120.f), two(-1.f / 720.f), two(2.f),   two(-1.f)};
+}
+template <int V>
+__device__ __forceinline__ Vf<V> both(const float2& c) {
+  Vf<V> o;
+#pragma unroll
+  for (int k = 0; k < V; ++k) o[k] = k & 1 ? c.y : c.x;
+  return o;
+}
+
+// The sigmoids share a reciprocal, 1 / ((1 + e^-r)(1 + e^-i)): the special
+// functions, 16 a clock and SM, are the first limit of these kernels, and this
+// leaves 5 of them an element.  So that the product stays finite r and i stop
+// at -44, and e^-44 (a little more, for the reciprocal's error) is taken off
+// the sigmoids again: a gate is exactly 0 there, at -infinity too, and off by
+// less than 2^-63 in front of it.  The subtraction saturates to [0, 1], which
+// makes a NaN 0, so u takes the reciprocal times 0 with it.
+constexpr float kGateLowest = -44.f;
+constexpr float kGateFloor = 7.79e-20f;  // e^-44 = 7.781e-20
+
+__device__ __forceinline__ float fma_sat(float a, float b, float c) {
+  float y;
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+template <int V>
 struct GateValues {
-  float s, g, a, m;
+  Vf<V> s, g, a, m, nan;  // nan: 0, or NaN where r or i is
 };
 
-__device__ __forceinline__ float fast_sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+// r and i at least kGateLowest.  IN_ROOT: m = sqrt(1 - a^2); else 1 - a^2.
+template <int V, bool IN_ROOT = true>
+__device__ __forceinline__ GateValues<V> gate_values(const GateConsts& c, const Vf<V>& r, const Vf<V>& i,
+                                                     const Vf<V>& decay) {
+  GateValues<V> o;
+  const Vf<V> one = both<V>(c.one), none = both<V>(c.none);
+  Vf<V> er = mul_v(r, both<V>(c.nlog2e)), ei = mul_v(i, both<V>(c.nlog2e));
+#pragma unroll
+  for (int k = 0; k < V; ++k) er[k] = ex2_approx(er[k]), ei[k] = ex2_approx(ei[k]);
+  er = add_v(er, one);
+  ei = add_v(ei, one);
+  Vf<V> inv = mul_v(er, ei);
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    inv[k] = rcp_approx(inv[k]);
+    o.s[k] = fma_sat(inv[k], ei[k], -kGateFloor);
+    o.g[k] = fma_sat(inv[k], er[k], -kGateFloor);
+  }
+  o.nan = inv;
+  const Vf<V> w = mul_v(decay, o.s);  // -l
+  // 1 - e^-w = w (1 - w/2 + w^2/6 - w^3/24 + w^4/120 - w^5/720); the next term
+  // is w^6/5040 < 5e-8 of it for w < 1/4
+  Vf<V> p = fma_v(w, both<V>(c.p6), both<V>(c.p5));
+  p = fma_v(w, p, both<V>(c.p4));
+  p = fma_v(w, p, both<V>(c.p3));
+  p = fma_v(w, p, both<V>(c.nhalf));
+  p = fma_v(w, p, one);
+  Vf<V> E = mul_v(w, p), far = mul_v(w, both<V>(c.nlog2e));
+#pragma unroll
+  for (int k = 0; k < V; ++k) far[k] = ex2_approx(far[k]);
+  const Vf<V> near_a = fma_v(E, none, one), far_E = fma_v(far, none, one);
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const bool near1 = w[k] < 0.25f;
+    E[k] = near1 ? E[k] : far_E[k];
+    o.a[k] = near1 ? near_a[k] : far[k];
+  }
+  o.m = mul_v(E, fma_v(E, none, both<V>(c.two)));
+  if constexpr (IN_ROOT)
+#pragma unroll
+    for (int k = 0; k < V; ++k) o.m[k] = sqrt_approx(o.m[k]);
+  return o;
+}
+// m g x, and NaN where a gate is
+template <int V>
+__device__ __forceinline__ Vf<V> gated_input(const GateValues<V>& v, const Vf<V>& m, const Vf<V>& x) {
+  return fma_v(v.nan, splat<V>(0.f), mul_v(mul_v(m, v.g), x));
+}
 
-__device__ __forceinline__ GateValues gate_values(float r, float i, float decay) {
-  GateValues o;
-  o.s = fast_sigmoid(r);
-  o.g = fast_sigmoid(i);
-  const float l = -decay * o.s;
-  // 1 - e^l = -l (1 + l/2 + l^2/6 + l^3/24 + l^4/120 + l^5/720); the next term
-  // is l^6/5040 < 5e-8 of it for |l| < 1/4
-  float p = fmaf(l, 1.f / 720.f, 1.f / 120.f);
-  p = fmaf(l, p, 1.f / 24.f);
-  p = fmaf(l, p, 1.f / 6.f);
-  p = fmaf(l, p, 0.5f);
-  p = fmaf(l, p, 1.f);
-  const float far = __expf(l);
-  const bool near1 = l > -0.25f;
-  const float E = near1 ? -l * p : 1.f - far;
-  o.a = near1 ? 1.f - E : far;
-  o.m = sqrtf(E * (2.f - E));
+template <int V>
+__device__ __forceinline__ Vf<V> lowest(Vf<V> v) {
+#pragma unroll
+  for (int k = 0; k < V; ++k) v[k] = max_nan(v[k], kGateLowest);
+  return v;
+}
+// Gates as they are in memory, at least kGateLowest (NaN stays).
+template <typename T, int V>
+__device__ __forceinline__ Vf<V> gate_input(Raw<T, V> raw) {
+  Vf<V> o;
+  if constexpr (sizeof(T) == 2 && V == 2) {
+    const float2 lowest = make_float2(kGateLowest, kGateLowest);
+    uint32_t w = raw;
+    if constexpr (std::is_same<T, __half>::value) {
+      const __half2 l = __float22half2_rn(lowest);
+      asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(w) : "r"(*reinterpret_cast<const uint32_t*>(&l)));
+    } else {
+      const __nv_bfloat162 l = __float22bfloat162_rn(lowest);
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(*reinterpret_cast<const uint32_t*>(&l)));
+    }
+    unpack<T, V>(w, o.v);
+  } else {
+    unpack<T, V>(raw, o.v);
+    o = lowest(o);
+  }
   return o;
 }
 
@@ -61,114 +155,577 @@ struct ScanArgs {
   const float* states_in;
   int N, C, packed, fill;
   long long L;
+  GateConsts consts;
 };
 
-// element (n, t, c) of an input
-template <typename T>
-__device__ __forceinline__ float scan_value(const ScanIn& in, const ScanArgs& a, int n, long long t, int c) {
-  const long long at = n * in.batch + t * in.token + c;
-  if (!in.scale) return to_f32<T>(static_cast<const T*>(in.p)[at]);
-  const int nblk = (a.C + ACT8_BLOCK - 1) / ACT8_BLOCK;
-  const long long row = static_cast<long long>(n) * a.L + t;
-  return static_cast<float>(static_cast<const signed char*>(in.p)[at]) *
-         act8_step(in.scale[row * nblk + c / ACT8_BLOCK]);
+// ---- one pass over time --------------------------------------------------
+//
+// A warp owns 32 * V neighbouring channels and kSteps tokens in a row, kept in
+// registers; a CTA is kScanWarps warps, one behind the other in time; a cluster
+// is up to eight CTAs one behind the other, and walks along a sequence in turns
+// of as many tokens as it holds.  A segment of tokens is the map
+// h -> P h + H (P the product of its a's, H its own end state), so per turn the
+// warps leave (P, H) in shared memory, the CTAs' maps go to every CTA of the
+// cluster through distributed shared memory, and once they are there every
+// thread knows the state in front of its own tokens.  The inputs are read once
+// and the outputs written once, and the order of the sums is fixed.  The
+// backward pass is the same walk from the end.
+//
+// A map that begins a sequence takes nothing from in front of it: P = -1 marks
+// it, and is tested rather than multiplied with, so that no NaN of one sequence
+// reaches the next.
+constexpr int kScanWarps = 8;
+constexpr int kScanThreads = 32 * kScanWarps;
+constexpr int kScanSteps = 8;
+constexpr int kScanMaxCluster = 8;
+static_assert(kScanWarps * kScanSteps == GATED_SCAN_STATE_EVERY, "a CTA's tokens begin at a kept state");
+
+template <int V>
+struct alignas(8 * V) ScanMap {
+  Vf<V> P, H;
+};
+template <int V>
+__device__ __forceinline__ ScanMap<V> no_map() {
+  return ScanMap<V>{splat<V>(1.f), splat<V>(0.f)};
 }
 
-constexpr int kScanThreads = 64;
+// h behind the map f.
+template <bool PACKED, int V>
+__device__ __forceinline__ Vf<V> follow(const ScanMap<V>& f, const Vf<V>& h) {
+  Vf<V> o = fma_v(f.P, h, f.H);
+  if (PACKED)
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = f.P[k] < 0.f ? f.H[k] : o[k];
+  return o;
+}
+// f, then g
+template <bool PACKED, int V>
+__device__ __forceinline__ ScanMap<V> then(const ScanMap<V>& f, const ScanMap<V>& g) {
+  ScanMap<V> o;
+  o.H = follow<PACKED>(g, f.H);
+  o.P = mul_v(f.P, g.P);
+  if (PACKED)
+#pragma unroll
+    for (int k = 0; k < V; ++k) o.P[k] = f.P[k] < 0.f || g.P[k] < 0.f ? -1.f : o.P[k];
+  return o;
+}
+// f, then a token: h -> a h + u
+template <bool PACKED, int V>
+__device__ __forceinline__ void then_token(ScanMap<V>& f, const Vf<V>& a, const Vf<V>& u) {
+  const Vf<V> P = mul_v(f.P, a);
+  f.H = fma_v(a, f.H, u);
+#pragma unroll
+  for (int k = 0; k < V; ++k) f.P[k] = PACKED && f.P[k] < 0.f ? -1.f : P[k];
+}
 
-// A thread a channel of a sequence, one token after the other.
-template <typename T>
-__global__ void __launch_bounds__(kScanThreads) gated_scan_kernel(const ScanArgs a) {
-  ptx::pdl_wait_prev();
-  const int c = blockIdx.x * kScanThreads + threadIdx.x, s = blockIdx.y;
-  if (c >= a.C) return;
-  T* y = static_cast<T*>(a.y);
-  const int n = a.packed ? 0 : s;
-  const long long row0 = static_cast<long long>(n) * a.L, blocks = (a.L + 63) / 64;
-  long long t0 = 0, t1 = a.L;
-  if (a.packed) {
-    t0 = max(0LL, min(a.L, static_cast<long long>(a.cu[s])));
-    t1 = max(t0, min(a.L, static_cast<long long>(a.cu[s + 1])));
-  }
-  const float decay = a.decay[c];
-  float h = a.h0 ? a.h0[static_cast<long long>(s) * a.C + c] : 0.f;
-  for (long long t = t0; t < t1; ++t) {
-    if (a.states && t % 64 == 0) a.states[(n * blocks + t / 64) * a.C + c] = t == t0 ? 0.f : h;
-    const GateValues v =
-        gate_values(scan_value<T>(a.r, a, n, t, c), scan_value<T>(a.i, a, n, t, c), decay);
-    h = fmaf(v.a, h, v.m * v.g * scan_value<T>(a.x, a, n, t, c));
-    y[(row0 + t) * a.C + c] = from_f32<T>(h);
-  }
-  if (a.h_last) a.h_last[static_cast<long long>(s) * a.C + c] = h;
-  if (a.packed && s == a.N - 1) {
-    for (long long t = t1; t < a.L; ++t) {
-      if (a.fill) y[t * a.C + c] = from_f32<T>(0.f);
-      if (a.states && t % 64 == 0) a.states[t / 64 * a.C + c] = 0.f;
+// V channels of kScanSteps rows of an input, loaded together: rows t0 + j for
+// the bits j of `used`.  The others are 0, or with GATE -infinity: a row whose
+// gate r is that, and whose x is 0, leaves the state exactly as it is.
+constexpr unsigned kScanAll = (1u << kScanSteps) - 1;
+
+template <typename T, int V, bool Q8, bool GATE>
+struct ScanRows {
+  using R = Raw<T, V>;
+  using R8 = typename RawVec<V>::type;
+  R raw[kScanSteps];
+  unsigned char byte[Q8 ? kScanSteps : 1];
+
+  __device__ __forceinline__ void load(const ScanIn& in, int n, long long L, int C, long long t0, int c, unsigned used) {
+    if (Q8 && in.scale) {
+      const signed char* p = static_cast<const signed char*>(in.p) + n * in.batch + t0 * in.token + c;
+      const int nblk = (C + ACT8_BLOCK - 1) / ACT8_BLOCK;
+      const unsigned char* sc = in.scale + (n * L + t0) * nblk + c / ACT8_BLOCK;
+#pragma unroll
+      for (int j = 0; j < kScanSteps; ++j) {
+        union {
+          R r;
+          R8 q;
+          signed char e[V];
+        } u;
+        u.r = R();
+#pragma unroll
+        for (int k = 0; k < V; ++k) u.e[k] = GATE ? -128 : 0;
+        byte[Q8 ? j : 0] = 254;  // -128 * 2^127
+        if (used >> j & 1) {
+          u.q = __ldg(reinterpret_cast<const R8*>(p + j * in.token));
+          byte[Q8 ? j : 0] = __ldg(sc + j * nblk);
+        }
+        raw[j] = u.r;
+      }
+      return;
+    }
+    const T* p = static_cast<const T*>(in.p) + n * in.batch + t0 * in.token + c;
+    if (used == kScanAll) {
+#pragma unroll
+      for (int j = 0; j < kScanSteps; ++j) raw[j] = load_raw<T, V>(p + j * in.token);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < kScanSteps; ++j) {
+      union {
+        R r;
+        T e[V];
+      } u;
+#pragma unroll
+      for (int k = 0; k < V; ++k) u.e[k] = from_f32<T>(GATE ? -INFINITY : 0.f);
+      raw[j] = u.r;
+      if (used >> j & 1) raw[j] = load_raw<T, V>(p + j * in.token);
     }
   }
-  if (a.packed && s == 0)
-    for (long long t = 0; t < t0; ++t) {
-      if (a.fill) y[t * a.C + c] = from_f32<T>(0.f);
-      if (a.states && t % 64 == 0) a.states[t / 64 * a.C + c] = 0.f;
+  __device__ __forceinline__ Vf<V> get(int j, const ScanIn& in) const {
+    Vf<V> o;
+    if (Q8 && in.scale) {
+      union {
+        R r;
+        signed char e[V];
+      } u;
+      u.r = raw[j];
+      const float step = act8_step(byte[Q8 ? j : 0]);
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = static_cast<float>(u.e[k]) * step;
+    } else {
+      unpack<T, V>(raw[j], o.v);
+    }
+    return o;
+  }
+};
+
+// What the tokens t0 .. t0 + STEPS - 1 are: bit j of `used` where token
+// t0 + j is in a sequence, of `first` and `last` where it begins or ends one;
+// lane j holds its sequence in `seq`.  Called by whole warps.
+struct ScanTokens {
+  unsigned used, first, last;
+  int seq;
+};
+
+template <int STEPS, bool PACKED>
+__device__ __forceinline__ ScanTokens scan_tokens(const ScanArgs& a, long long t0) {
+  ScanTokens k = {0, 0, 0, 0};
+  if constexpr (PACKED) {
+    const int lane = threadIdx.x & 31;
+    const long long t = t0 + lane;
+    bool used = false, first = false, last = false;
+    if (lane < STEPS && t >= 0 && t < a.L) {
+      k.seq = seq_of_row(a.cu, a.N, t);
+      if (k.seq < a.N) {
+        used = true;
+        first = t == 0 || __ldg(a.cu + k.seq) == t;
+        last = __ldg(a.cu + k.seq + 1) == t + 1 || t + 1 == a.L;
+      }
+    }
+    k.used = __ballot_sync(0xffffffffu, used);
+    k.first = __ballot_sync(0xffffffffu, first);
+    k.last = __ballot_sync(0xffffffffu, last);
+  } else {
+    const long long left = t0 < 0 ? 0 : a.L - t0;
+    k.used = left >= STEPS ? (1u << STEPS) - 1 : left > 0 ? (1u << left) - 1 : 0;
+  }
+  return k;
+}
+
+// Channels c .. c + width - 1 (V at most) of row s of [rows, C] states; zeros
+// without them.
+template <int V>
+__device__ __forceinline__ Vf<V> scan_initial(const float* h0, long long s, int C, int c, int width) {
+  Vf<V> h;
+#pragma unroll
+  for (int k = 0; k < V; ++k) h[k] = h0 && k < width ? __ldg(h0 + s * C + c + k) : 0.f;
+  return h;
+}
+template <int V>
+__device__ __forceinline__ void put_state(float* h, long long s, int C, int c, int width, const Vf<V>& v) {
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (k < width) h[s * C + c + k] = v[k];
+}
+template <typename T, int V, bool ALIGNED>
+__device__ __forceinline__ void put_row(T* p, int width, const Vf<V>& v) {
+  if constexpr (ALIGNED) {
+    store_vec<T, V>(p, v.v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (k < width) p[k] = from_f32<T>(v[k]);
+  }
+}
+// What sequences without a token pass on: `from` (or zeros) into `to`.
+template <int V>
+__device__ __forceinline__ void pass_empty(const ScanArgs& a, const float* from, float* to, int first, int step, int c,
+                                           int width) {
+  if (width <= 0 || !to) return;
+  for (int s = first; s < a.N; s += step)
+    if (__ldg(a.cu + s) >= __ldg(a.cu + s + 1))
+      put_state<V>(to, s, a.C, c, width, scan_initial<V>(from, s, a.C, c, width));
+}
+
+// The maps of a turn: the CTA's warps', and one of each CTA of the cluster.
+// Two of each, for a warp may be a turn ahead of another.
+template <int V>
+struct ScanShared {
+  ScanMap<V> warp[2][kScanWarps][32];
+  ScanMap<V> cta[2][kScanMaxCluster][32];
+};
+
+__device__ __forceinline__ int cluster_rank() {
+  int r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ int cluster_size() {
+  int r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// The cluster's barrier in two halves.  The warp that wrote to other CTAs arrives
+// with `wrote`, a release; that waits for all of the thread's accesses, its loads
+// among them, so the other warps arrive without.
+__device__ __forceinline__ void cluster_arrive(bool wrote) {
+  if (wrote) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  else asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Stores a map to the same place in CTA `rank`'s shared memory.
+template <int V>
+__device__ __forceinline__ void store_remote(ScanMap<V>* p, int rank, const ScanMap<V>& m) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(p)), "r"(rank));
+  if constexpr (V == 2)
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(m.P[0]), "f"(m.P[1]), "f"(m.H[0]),
+                 "f"(m.H[1])
+                 : "memory");
+  else
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(m.P[0]), "f"(m.H[0]) : "memory");
+}
+
+// Takes each warp's map of this turn (`mine`) and the state in front of the
+// cluster's turn (`carry`); gives the state in front of the warp's own tokens
+// and moves `carry` behind the turn.  b: the turn's parity.  `order` is the
+// warp's place in time among the CTA's (0 first), `rank` the CTA's among the
+// cluster's.  Every thread of the cluster calls it; inactive channels take part
+// with whatever they hold.  `load` loads the next turn's rows: before the
+// exchange, but in the warp that writes to the other CTAs only behind its
+// release.
+template <bool PACKED, int V, typename Load>
+__device__ __forceinline__ Vf<V> scan_exchange(ScanShared<V>& sh, int b, int order, int rank, int ctas,
+                                               const ScanMap<V>& mine, Vf<V>& carry, Load&& load) {
+  const int lane = threadIdx.x & 31;
+  const bool writer = ctas > 1 && order == kScanWarps - 1;
+  Vf<V> before;
+  sh.warp[b][order][lane] = mine;
+  if (!writer) load();
+  __syncthreads();
+  ScanMap<V> front = no_map<V>();  // the CTA's warps in front of this one
+#pragma unroll
+  for (int w = 0; w < kScanWarps - 1; ++w)
+    if (w < order) front = then<PACKED>(front, sh.warp[b][w][lane]);
+  if (ctas > 1) {
+    if (writer) {
+      const ScanMap<V> all = then<PACKED>(front, mine);
+      for (int r = 0; r < ctas; ++r) store_remote<V>(&sh.cta[b][rank][lane], r, all);
+      cluster_arrive(true);
+      load();
+    } else {
+      cluster_arrive(false);
+    }
+    cluster_wait();
+    before = carry;
+#pragma unroll
+    for (int r = 0; r < kScanMaxCluster; ++r)
+      if (r < ctas) {
+        carry = follow<PACKED>(sh.cta[b][r][lane], carry);
+        if (r < rank) before = carry;
+      }
+    before = follow<PACKED>(front, before);
+  } else {
+    before = follow<PACKED>(front, carry);
+    ScanMap<V> all = no_map<V>();
+#pragma unroll
+    for (int w = 0; w < kScanWarps; ++w) all = then<PACKED>(all, sh.warp[b][w][lane]);
+    carry = follow<PACKED>(all, carry);
+  }
+  return before;
+}
+
+// ---- rows in shared memory ------------------------------------------------
+//
+// Each warp copies its own rows of the next turn there while it works on this
+// one: 16 bytes an instruction and no registers, and only the warp itself waits
+// for them.  Rows that are not 16-byte aligned (ALIGNED false) go element by
+// element through registers.
+template <typename T, int STEPS>
+struct alignas(16) ScanTile {
+  T v[STEPS][64];
+};
+
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
+               : "memory");  // zeros where it is not
+}
+__device__ __forceinline__ void copies_done() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+}
+
+// Rows t0 .. t0 + STEPS - 1, channels c0 .. c0 + 63 of an input; zeros outside.
+// Whole warps, behind their last use of the tile.
+template <typename T, int STEPS, bool ALIGNED>
+__device__ __forceinline__ void load_tile(ScanTile<T, STEPS>& tile, const ScanIn& in, int n, long long L, int C,
+                                          long long t0, int c0) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (ALIGNED) {
+    constexpr int kPer = 16 / sizeof(T), kRow = 64 / kPer, kRows = 32 / kRow;  // elements a copy, copies a row, rows at once
+    const int row = lane / kRow, col = lane % kRow * kPer;
+    const bool in_c = c0 + col < C;
+    const T* p = static_cast<const T*>(in.p) + n * in.batch + (t0 + row) * in.token + c0 + col;
+    const long long left = L - t0 - row;
+#pragma unroll
+    for (int j = 0; j < STEPS; j += kRows) {
+      const bool there = in_c && j < left;
+      copy16(&tile.v[j + row][col], there ? p + j * in.token : static_cast<const T*>(in.p), there);
+    }
+  } else {
+    const T* p = static_cast<const T*>(in.p) + n * in.batch + t0 * in.token + c0;
+    for (int j = 0; j < STEPS; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int col = lane + 32 * k;
+        tile.v[j][col] = t0 + j < L && c0 + col < C ? p[j * in.token + col] : from_f32<T>(0.f);
+      }
+  }
+}
+
+// Rows that are in no sequence leave the state exactly as it is: their gate r
+// becomes -infinity and everything else 0.  Whole warps; `used`: bit j is row j.
+template <typename T, int STEPS>
+__device__ __forceinline__ void void_rows(ScanTile<T, STEPS>& tile, unsigned used, float with) {
+  const int lane = threadIdx.x & 31;
+  for (int j = 0; j < STEPS; ++j)
+    if (!(used >> j & 1)) tile.v[j][lane] = tile.v[j][lane + 32] = from_f32<T>(with);
+}
+
+template <typename T, int STEPS>
+__device__ __forceinline__ Raw<T, 2> row_pair(const ScanTile<T, STEPS>& tile, int j, int lane) {
+  return *reinterpret_cast<const Raw<T, 2>*>(&tile.v[j][2 * lane]);
+}
+
+// Tokens of a warp in the forward pass: the maps of a turn cost as much however
+// many there are, but a and u of each stay in registers.
+constexpr int kForwardSteps = 16;
+
+template <typename T>
+struct ForwardShared {
+  ScanShared<2> maps;
+  struct {
+    ScanTile<T, kForwardSteps> x, r, i;
+  } warp[kScanWarps];
+};
+
+template <typename T, bool PACKED, bool ALIGNED>
+__global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const ScanArgs a) {
+  constexpr int STEPS = kForwardSteps, V = 2;
+  constexpr unsigned kAll = (1u << STEPS) - 1;
+  extern __shared__ __align__(128) unsigned char smem[];
+  ForwardShared<T>& sh = *reinterpret_cast<ForwardShared<T>*>(smem);
+  ptx::pdl_wait_prev();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = cluster_rank(), ctas = cluster_size();
+  const int c0 = static_cast<int>(blockIdx.x / ctas) * 64, c = c0 + lane * V, n = blockIdx.y;
+  // with rows that are not aligned C may be odd: the last channel stands alone
+  const int width = min(V, a.C - c);
+  const bool in = width > 0;
+  auto& tile = sh.warp[warp];
+  T* y = static_cast<T*>(a.y) + (n * a.L) * a.C + c;
+  const long long blocks = (a.L + GATED_SCAN_STATE_EVERY - 1) / GATED_SCAN_STATE_EVERY;
+  const Vf<V> decay = scan_initial<V>(a.decay, 0, a.C, c, width);
+  Vf<V> carry = PACKED ? splat<V>(0.f) : scan_initial<V>(a.h0, n, a.C, c, width);
+  if (PACKED) pass_empty<V>(a, a.h0, a.h_last, rank * kScanWarps + warp, ctas * kScanWarps, c, width);
+  if (ctas > 1) cluster_arrive(false), cluster_wait();  // every CTA runs before another writes to its shared memory
+  const long long span = static_cast<long long>(ctas) * kScanWarps * STEPS;
+  const int turns = static_cast<int>((a.L + span - 1) / span);
+  long long t0 = (rank * kScanWarps + warp) * STEPS;
+  const auto load = [&](long long t) {
+    load_tile<T, STEPS, ALIGNED>(tile.r, a.r, n, a.L, a.C, t, c0);
+    load_tile<T, STEPS, ALIGNED>(tile.i, a.i, n, a.L, a.C, t, c0);
+    load_tile<T, STEPS, ALIGNED>(tile.x, a.x, n, a.L, a.C, t, c0);
+  };
+  load(t0);
+  for (int turn = 0; turn < turns; ++turn, t0 += span) {
+    const ScanTokens tok = scan_tokens<STEPS, PACKED>(a, t0);
+    copies_done();
+    if (tok.used != kAll) {
+      void_rows(tile.r, tok.used, -INFINITY);
+      void_rows(tile.i, tok.used, 0.f);
+      void_rows(tile.x, tok.used, 0.f);
+      __syncwarp();
+    }
+    Vf<V> av[STEPS], u[STEPS];
+    ScanMap<V> mine = no_map<V>();
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      const GateValues<V> g = gate_values<V>(a.consts, gate_input<T, V>(row_pair(tile.r, j, lane)),
+                                             gate_input<T, V>(row_pair(tile.i, j, lane)), decay);
+      Vf<V> x;
+      unpack<T, V>(row_pair(tile.x, j, lane), x.v);
+      u[j] = gated_input<V>(g, g.m, x);
+      av[j] = g.a;
+      if (PACKED && (tok.first >> j & 1))
+        mine = ScanMap<V>{splat<V>(-1.f), scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, width)};
+      then_token<PACKED>(mine, av[j], u[j]);
+    }
+    __syncwarp();
+    Vf<V> h = scan_exchange<PACKED, V>(sh.maps, turn & 1, warp, rank, ctas, mine, carry, [&] { load(t0 + span); });
+    if (in && a.states && t0 < a.L && t0 % GATED_SCAN_STATE_EVERY == 0)
+      put_state<V>(a.states, n * blocks + t0 / GATED_SCAN_STATE_EVERY, a.C, c, width, h);
+    T* out = y + t0 * a.C;
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      if (PACKED && (tok.first >> j & 1))
+        h = scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, width);
+      h = fma_v(av[j], h, u[j]);
+      if (in && (tok.used >> j & 1)) put_row<T, V, ALIGNED>(out + static_cast<long long>(j) * a.C, width, h);
+      else if (PACKED && in && a.fill && t0 + j < a.L)
+        put_row<T, V, ALIGNED>(out + static_cast<long long>(j) * a.C, width, splat<V>(0.f));
+      if (PACKED && (tok.last >> j & 1)) {
+        const int s = __shfl_sync(0xffffffffu, tok.seq, j);
+        if (in && a.h_last) put_state<V>(a.h_last, s, a.C, c, width, h);
+      }
+    }
+  }
+  copies_done();
+  if (!PACKED && in && a.h_last && rank == 0 && warp == 0) put_state<V>(a.h_last, n, a.C, c, width, carry);
+}
+
+template <typename T, int V, bool PACKED, bool Q8>
+__global__ void __launch_bounds__(kScanThreads, 2) gated_scan_grad_kernel(const ScanArgs a) {
+  __shared__ ScanShared<V> sh;
+  __shared__ ScanMap<V> ahead[2][kScanWarps][32];
+  ptx::pdl_wait_prev();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = cluster_rank(), ctas = cluster_size();
+  const int c = (static_cast<int>(blockIdx.x / ctas) * 32 + lane) * V, n = blockIdx.y;
+  const bool in = c < a.C;
+  const long long blocks = (a.L + GATED_SCAN_STATE_EVERY - 1) / GATED_SCAN_STATE_EVERY;
+  Vf<V> decay, dd = splat<V>(0.f);
+#pragma unroll
+  for (int k = 0; k < V; ++k) decay[k] = in ? __ldg(a.decay + c + k) : 0.f;
+  Vf<V> carry = PACKED ? splat<V>(0.f) : scan_initial<V>(a.dh_last, n, a.C, c, in * V);
+  if (PACKED) pass_empty<V>(a, a.dh_last, a.dh0, rank * kScanWarps + warp, ctas * kScanWarps, c, in * V);
+  if (ctas > 1) cluster_arrive(false), cluster_wait();  // every CTA runs before another writes to its shared memory
+  const long long span = static_cast<long long>(ctas) * GATED_SCAN_STATE_EVERY;
+  const int turns = static_cast<int>((a.L + span - 1) / span);
+  for (int turn = turns - 1; turn >= 0; --turn) {
+    const long long block = turn * static_cast<long long>(ctas) + rank, begin = block * GATED_SCAN_STATE_EVERY;
+    const long long t0 = begin + warp * kScanSteps;
+    const ScanTokens tok = scan_tokens<kScanSteps, PACKED>(a, t0);
+    const unsigned used = in ? tok.used : 0;
+    ScanRows<T, V, Q8, false> x, i;
+    ScanRows<T, V, Q8, true> r;
+    ScanRows<T, V, false, false> dy;
+    r.load(a.r, n, a.L, a.C, t0, c, used);
+    i.load(a.i, n, a.L, a.C, t0, c, used);
+    x.load(a.x, n, a.L, a.C, t0, c, used);
+    dy.load(a.dy, n, a.L, a.C, t0, c, used);
+    // the state in front of the CTA's tokens
+    const bool start = !PACKED && begin == 0;
+    Vf<V> h = scan_initial<V>(start ? a.h0 : a.states_in, start ? n : n * blocks + block, a.C, c, in && begin < a.L ? V : 0);
+    Vf<V> av[kScanSteps], s[kScanSteps], g[kScanSteps], m2[kScanSteps];  // m2 = 1 - a^2
+    ScanMap<V> fwd = no_map<V>(), bwd = no_map<V>();
+#pragma unroll
+    for (int j = 0; j < kScanSteps; ++j) {
+      const GateValues<V> gv = gate_values<V, false>(a.consts, lowest(r.get(j, a.r)), lowest(i.get(j, a.i)), decay);
+      s[j] = gv.s;
+      g[j] = gv.g;
+      m2[j] = gv.m;
+      av[j] = gv.a;
+      Vf<V> m;
+#pragma unroll
+      for (int k = 0; k < V; ++k) m[k] = sqrt_approx(m2[j][k]);
+      if (PACKED && (tok.first >> j & 1))
+        fwd = ScanMap<V>{splat<V>(-1.f), scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, in * V)};
+      then_token<PACKED>(fwd, av[j], gated_input<V>(gv, m, x.get(j, a.x)));
+    }
+#pragma unroll
+    for (int j = kScanSteps - 1; j >= 0; --j) {
+      if (PACKED && (tok.last >> j & 1))
+        bwd = ScanMap<V>{splat<V>(-1.f), scan_initial<V>(a.dh_last, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, in * V)};
+      then_token<PACKED>(bwd, av[j], mul_v(av[j], dy.get(j, a.dy)));
+    }
+    // forward only within the CTA, whose first state is kept; backward through
+    // the cluster, whose last warp comes first (the barriers inside cover both)
+    const int b = turn & 1;
+    ahead[b][warp][lane] = fwd;
+    Vf<V> G = scan_exchange<PACKED, V>(sh, b, kScanWarps - 1 - warp, ctas - 1 - rank, ctas, bwd, carry, [] {});
+#pragma unroll
+    for (int w = 0; w < kScanWarps - 1; ++w)
+      if (w < warp) h = follow<PACKED>(ahead[b][w][lane], h);
+    Vf<V> hp[kScanSteps];  // the state in front of each token
+#pragma unroll
+    for (int j = 0; j < kScanSteps; ++j) {
+      if (PACKED && (tok.first >> j & 1))
+        h = scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, in * V);
+      hp[j] = h;
+      Vf<V> m;
+#pragma unroll
+      for (int k = 0; k < V; ++k) m[k] = sqrt_approx(m2[j][k]);
+      h = fma_v(av[j], h, mul_v(mul_v(m, g[j]), x.get(j, a.x)));
+    }
+    const long long row = (n * a.L + t0) * a.C + c;
+    Vf<V> part = splat<V>(0.f);
+#pragma unroll
+    for (int j = kScanSteps - 1; j >= 0; --j) {
+      if (PACKED && (tok.last >> j & 1))
+        G = scan_initial<V>(a.dh_last, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, in * V);
+      const Vf<V> xv = x.get(j, a.x), one = splat<V>(1.f);
+      Vf<V> over;  // 1 / m, 0 where a = 1
+#pragma unroll
+      for (int k = 0; k < V; ++k) over[k] = m2[j][k] > 0.f ? rsqrt_approx(m2[j][k]) : m2[j][k];
+      const Vf<V> m = mul_v(m2[j], over);
+      const Vf<V> whole = add_v(dy.get(j, a.dy), G), vx = mul_v(g[j], xv), Gm = mul_v(whole, m);
+      G = mul_v(av[j], whole);
+      const Vf<V> back = mul_v(mul_v(av[j], vx), over);
+      const Vf<V> dl = mul_v(G, add_v(hp[j], neg_v(back))), sdl = mul_v(s[j], dl);
+      const Vf<V> dx = mul_v(Gm, g[j]), di = mul_v(mul_v(Gm, vx), fma_v(g[j], splat<V>(-1.f), one));
+      const Vf<V> dr = mul_v(mul_v(neg_v(decay), sdl), fma_v(s[j], splat<V>(-1.f), one));
+      const long long at = row + static_cast<long long>(j) * a.C;
+      if (used >> j & 1) {
+        part = add_v(part, sdl);
+        store_vec<T, V>(static_cast<T*>(a.dx) + at, dx.v);
+        store_vec<T, V>(static_cast<T*>(a.dr) + at, dr.v);
+        store_vec<T, V>(static_cast<T*>(a.di) + at, di.v);
+      } else if (PACKED && in && a.fill && t0 + j < a.L) {
+        store_zero<T, V>(static_cast<T*>(a.dx) + at);
+        store_zero<T, V>(static_cast<T*>(a.dr) + at);
+        store_zero<T, V>(static_cast<T*>(a.di) + at);
+      }
+      if (PACKED && (tok.first >> j & 1)) {
+        const int q = __shfl_sync(0xffffffffu, tok.seq, j);
+        if (in && a.dh0) put_state<V>(a.dh0, q, a.C, c, V, G);
+      }
+    }
+    dd = add_v(dd, part);
+  }
+  if (!PACKED && in && a.dh0 && rank == 0 && warp == 0) put_state<V>(a.dh0, n, a.C, c, V, carry);
+  // ddecay: the CTA's warps in order
+  __syncthreads();
+  float* sums = &sh.warp[0][0][0].P[0];
+#pragma unroll
+  for (int k = 0; k < V; ++k) sums[(warp * V + k) * 32 + lane] = dd[k];
+  __syncthreads();
+  if (warp == 0 && in)
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kScanWarps; ++w) sum -= sums[(w * V + k) * 32 + lane];
+      a.part[(static_cast<long long>(n) * ctas + rank) * a.C + c + k] = sum;
     }
 }
 
-// A thread a channel of a sequence: blocks of 64 rows from the last to the
-// first, the states of each recomputed from the one in front of it.
-template <typename T>
-__global__ void __launch_bounds__(kScanThreads) gated_scan_grad_kernel(const ScanArgs a) {
+// ddecay: the partial sums [n][C] added in order.
+__global__ void __launch_bounds__(64) gated_scan_sum_kernel(const float* __restrict__ part, float* out, int n, int C) {
   ptx::pdl_wait_prev();
-  const int c = blockIdx.x * kScanThreads + threadIdx.x, s = blockIdx.y;
-  if (c >= a.C) return;
-  T *dx = static_cast<T*>(a.dx), *dr = static_cast<T*>(a.dr), *di = static_cast<T*>(a.di);
-  const int n = a.packed ? 0 : s;
-  const long long row0 = static_cast<long long>(n) * a.L, blocks = (a.L + 63) / 64;
-  long long t0 = 0, t1 = a.L;
-  if (a.packed) {
-    t0 = max(0LL, min(a.L, static_cast<long long>(a.cu[s])));
-    t1 = max(t0, min(a.L, static_cast<long long>(a.cu[s + 1])));
-  }
-  const long long sc = static_cast<long long>(s) * a.C + c;
-  const float decay = a.decay[c];
-  float carry = a.dh_last ? a.dh_last[sc] : 0.f, sum = 0.f;
-  float h[65];
-  for (long long end = t1; end > t0;) {
-    const long long begin = max(t0, (end - 1) / 64 * 64);
-    h[0] = begin == t0 ? (a.h0 ? a.h0[sc] : 0.f) : a.states_in[(n * blocks + begin / 64) * a.C + c];
-    for (long long t = begin; t < end; ++t) {
-      const GateValues v =
-          gate_values(scan_value<T>(a.r, a, n, t, c), scan_value<T>(a.i, a, n, t, c), decay);
-      h[t - begin + 1] = fmaf(v.a, h[t - begin], v.m * v.g * scan_value<T>(a.x, a, n, t, c));
-    }
-    float part = 0.f;
-    for (long long t = end - 1; t >= begin; --t) {
-      const GateValues v =
-          gate_values(scan_value<T>(a.r, a, n, t, c), scan_value<T>(a.i, a, n, t, c), decay);
-      const float x = scan_value<T>(a.x, a, n, t, c), G = scan_value<T>(a.dy, a, n, t, c) + carry;
-      carry = v.a * G;
-      const float back = v.m > 0.f ? v.a * v.g * x / v.m : 0.f;
-      const float dl = carry * (h[t - begin] - back);
-      const long long at = (row0 + t) * a.C + c;
-      dx[at] = from_f32<T>(G * v.m * v.g);
-      di[at] = from_f32<T>(G * v.m * x * v.g * (1.f - v.g));
-      dr[at] = from_f32<T>(-decay * dl * v.s * (1.f - v.s));
-      part = fmaf(-v.s, dl, part);
-    }
-    sum += part;
-    end = begin;
-  }
-  if (a.dh0) a.dh0[sc] = carry;
-  a.part[sc] = sum;
-  if (a.packed && a.fill && s == a.N - 1)
-    for (long long t = t1; t < a.L; ++t) dx[t * a.C + c] = dr[t * a.C + c] = di[t * a.C + c] = from_f32<T>(0.f);
-  if (a.packed && a.fill && s == 0)
-    for (long long t = 0; t < t0; ++t) dx[t * a.C + c] = dr[t * a.C + c] = di[t * a.C + c] = from_f32<T>(0.f);
-}
-
-// ddecay: the partial sums added in order.
-__global__ void __launch_bounds__(kScanThreads) gated_scan_sum_kernel(const float* part, float* out, int n, int C) {
-  ptx::pdl_wait_prev();
-  const int c = blockIdx.x * kScanThreads + threadIdx.x;
+  const int c = blockIdx.x * 64 + threadIdx.x;
   if (c >= C) return;
   float sum = 0.f;
   for (int k = 0; k < n; ++k) sum += part[static_cast<long long>(k) * C + c];
@@ -183,6 +740,7 @@ struct ScanStepArgs {
   void* y;
   int B, slots, C, fill;
   long long xs, rs, is;
+  GateConsts consts;
 };
 
 constexpr int kStepThreads = 128;
@@ -202,21 +760,18 @@ __global__ void __launch_bounds__(kStepThreads) gated_scan_step_kernel(const Sca
     if (a.fill) store_zero<T, V>(y + static_cast<long long>(b) * a.C);
     return;
   }
-  float decay[V], h[V];
+  Vf<V> decay, h;
   float* hp = a.h + static_cast<long long>(slot) * a.C + c;
 #pragma unroll
   for (int k = 0; k < V; ++k) decay[k] = __ldg(a.decay + c + k), h[k] = hp[k];
   do {
-    float x[V], r[V], i[V];
-    unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.x) + b * a.xs + c), x);
-    unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.r) + b * a.rs + c), r);
-    unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.i) + b * a.is + c), i);
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const GateValues v = gate_values(r[k], i[k], decay[k]);
-      h[k] = fmaf(v.a, h[k], v.m * v.g * x[k]);
-    }
-    store_vec<T, V>(y + static_cast<long long>(b) * a.C, h);
+    Vf<V> x, r, i;
+    unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.x) + b * a.xs + c), x.v);
+    unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.r) + b * a.rs + c), r.v);
+    unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.i) + b * a.is + c), i.v);
+    const GateValues<V> v = gate_values<V>(a.consts, lowest(r), lowest(i), decay);
+    h = fma_v(v.a, h, gated_input<V>(v, v.m, x));
+    store_vec<T, V>(y + static_cast<long long>(b) * a.C, h.v);
     if (!(others & 2)) break;
     for (++b; b < a.B && __ldg(a.index + b) != slot;) ++b;
   } while (b < a.B);

@@ -70,6 +70,112 @@ __device__ __forceinline__ void store_zero(T* p) {
   store_vec<T, V>(p, z);
 }
 
+// ---- V fp32 values at once ----------------------------------------------
+// Two are one packed instruction (fma.rn.f32x2 and its kin issue once for two
+// channels); each rounds as its scalar form does.
+template <int V>
+struct Vf {
+  float v[V];
+  __device__ __forceinline__ float& operator[](int k) { return v[k]; }
+  __device__ __forceinline__ const float& operator[](int k) const { return v[k]; }
+};
+
+template <int V>
+__device__ __forceinline__ Vf<V> splat(float x) {
+  Vf<V> o;
+#pragma unroll
+  for (int k = 0; k < V; ++k) o[k] = x;
+  return o;
+}
+
+__device__ __forceinline__ uint64_t pack2(const float* v) {
+  uint64_t o;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(o) : "f"(v[0]), "f"(v[1]));
+  return o;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float* v) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v[0]), "=f"(v[1]) : "l"(x));
+}
+
+template <int V>
+__device__ __forceinline__ Vf<V> fma_v(const Vf<V>& a, const Vf<V>& b, const Vf<V>& c) {
+  Vf<V> o;
+#pragma unroll
+  for (int k = 0; k + 1 < V; k += 2) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pack2(a.v + k)), "l"(pack2(b.v + k)), "l"(pack2(c.v + k)));
+    unpack2(d, o.v + k);
+  }
+  if constexpr (V & 1) o[V - 1] = fmaf(a[V - 1], b[V - 1], c[V - 1]);
+  return o;
+}
+template <int V>
+__device__ __forceinline__ Vf<V> mul_v(const Vf<V>& a, const Vf<V>& b) {
+  Vf<V> o;
+#pragma unroll
+  for (int k = 0; k + 1 < V; k += 2) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pack2(a.v + k)), "l"(pack2(b.v + k)));
+    unpack2(d, o.v + k);
+  }
+  if constexpr (V & 1) o[V - 1] = a[V - 1] * b[V - 1];
+  return o;
+}
+template <int V>
+__device__ __forceinline__ Vf<V> add_v(const Vf<V>& a, const Vf<V>& b) {
+  Vf<V> o;
+#pragma unroll
+  for (int k = 0; k + 1 < V; k += 2) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pack2(a.v + k)), "l"(pack2(b.v + k)));
+    unpack2(d, o.v + k);
+  }
+  if constexpr (V & 1) o[V - 1] = a[V - 1] + b[V - 1];
+  return o;
+}
+template <int V>
+__device__ __forceinline__ Vf<V> neg_v(const Vf<V>& a) {
+  Vf<V> o;
+#pragma unroll
+  for (int k = 0; k < V; ++k) o[k] = -a[k];
+  return o;
+}
+
+// The hardware's approximations, subnormals taken as zero: 2^x (2 ulp), 1 / x
+// (1 ulp), sqrt(x) (2^-23).
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// NaN where either is (fminf and fmaxf would drop it)
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
 // The step of a checkpoint's block: 2^(byte - 127), NaN for 255 and 0 for 0
 // (whose elements are all 0).
 __device__ __forceinline__ float act8_step(unsigned char s) {

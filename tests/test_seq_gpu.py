@@ -422,7 +422,11 @@ def test_gated_scan_gates_at_their_ends(cf):
         grads = cf.gated_scan_grad(*d, torch.ones_like(d[0]), states, h0=h0.cuda())
         for t in grads:
             assert torch.isfinite(t).all()
-        assert (grads[1][..., 1:4] == 0).all() and (grads[0][..., 1:3] == 0).all() and (grads[4][:, 1] == 70).all()
+        assert (grads[1][..., 1:3] == 0).all() and (grads[0][..., 1:3] == 0).all() and (grads[4][:, 1] == 70).all()
+        # r = inf: s is a reciprocal (1 ulp) times its own argument (half an ulp), so 1 - s is at most 2^-22, and
+        # |dr| = decay |dl| s (1 - s) with |dl| <= a |G| (|h| + a g |x| / m): a = e^-1/2, m = 0.795, |G| <= 1 / (1 - a)
+        # = 2.54, |g x| <= 5, |h| <= |h0| + m |g x| / (1 - a) <= 11.1: |dl| <= 0.607 * 2.54 * (11.1 + 3.9) = 23.2
+        assert x.abs().max() <= 5 and (grads[1][..., 3].float().abs() <= 0.5 * 23.2 * 2 ** -22).all()
 
 
 def test_gated_scan_continues_from_its_state(cf):
