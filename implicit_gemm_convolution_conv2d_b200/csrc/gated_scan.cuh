@@ -452,7 +452,8 @@ __device__ __forceinline__ Vf<V> scan_exchange(ScanShared<V>& sh, int b, int ord
 // Each warp copies its own rows of the next turn there while it works on this
 // one: 16 bytes an instruction and no registers, and only the warp itself waits
 // for them.  Rows that are not 16-byte aligned (ALIGNED false) go element by
-// element through registers.
+// element through registers, at the end of a turn when these are free: 8192
+// rows of 333 channels take 49 us, against 103 beside the turn's own values.
 template <typename T, int STEPS>
 struct alignas(16) ScanTile {
   T v[STEPS][64];
@@ -467,33 +468,50 @@ __device__ __forceinline__ void copies_done() {
   __syncwarp();
 }
 
-// Rows t0 .. t0 + STEPS - 1, channels c0 .. c0 + 63 of an input; zeros outside.
-// Whole warps, behind their last use of the tile.
+// Walks along an input, a warp's STEPS rows of 64 channels a turn, zeros outside
+// of it.  The address of the lane's first element moves on by addition.
 template <typename T, int STEPS, bool ALIGNED>
-__device__ __forceinline__ void load_tile(ScanTile<T, STEPS>& tile, const ScanIn& in, int n, long long L, int C,
-                                          long long t0, int c0) {
-  const int lane = threadIdx.x & 31;
-  if constexpr (ALIGNED) {
-    constexpr int kPer = 16 / sizeof(T), kRow = 64 / kPer, kRows = 32 / kRow;  // elements a copy, copies a row, rows at once
-    const int row = lane / kRow, col = lane % kRow * kPer;
-    const bool in_c = c0 + col < C;
-    const T* p = static_cast<const T*>(in.p) + n * in.batch + (t0 + row) * in.token + c0 + col;
-    const long long left = L - t0 - row;
-#pragma unroll
-    for (int j = 0; j < STEPS; j += kRows) {
-      const bool there = in_c && j < left;
-      copy16(&tile.v[j + row][col], there ? p + j * in.token : static_cast<const T*>(in.p), there);
-    }
-  } else {
-    const T* p = static_cast<const T*>(in.p) + n * in.batch + t0 * in.token + c0;
-    for (int j = 0; j < STEPS; ++j)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int col = lane + 32 * k;
-        tile.v[j][col] = t0 + j < L && c0 + col < C ? p[j * in.token + col] : from_f32<T>(0.f);
-      }
+struct TileWalk {
+  static constexpr int kPer = 16 / sizeof(T), kRow = 64 / kPer, kRows = 32 / kRow;  // elements a copy, copies a row, rows at once
+  const T* p;       // of the lane's first row and channel
+  long long token;  // elements from row to row
+
+  // from row t0 on; `width` channels from c0 on are there
+  __device__ __forceinline__ void start(const ScanIn& in, int n, long long t0, int c0) {
+    const int lane = threadIdx.x & 31;
+    token = in.token;
+    p = static_cast<const T*>(in.p) + n * in.batch + c0 + t0 * token;
+    if constexpr (ALIGNED) p += lane / kRow * token + lane % kRow * kPer;
   }
-}
+  // Copies the rows into `tile`: `rows` of them are there (any number: none
+  // below 1, all from STEPS on).  Whole warps, behind their last use of the tile.
+  __device__ __forceinline__ void load(ScanTile<T, STEPS>& tile, int rows, int width) const {
+    const int lane = threadIdx.x & 31;
+    if constexpr (ALIGNED) {
+      const int row = lane / kRow, col = lane % kRow * kPer;
+      const int mine = col < width ? rows - row : 0;
+      T* to = &tile.v[row][col];
+      const T* from = p;
+#pragma unroll
+      for (int j = 0; j < STEPS; j += kRows) {
+        copy16(to + j * 64, from, j < mine);
+        if (j + kRows < mine) from += kRows * token;  // never behind the last row
+      }
+    } else {
+      T v[STEPS][2];  // loaded together
+      const T* from = p + lane;
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j) {
+        v[j][0] = j < rows && lane < width ? from[0] : from_f32<T>(0.f);
+        v[j][1] = j < rows && lane + 32 < width ? from[32] : from_f32<T>(0.f);
+        from += token;
+      }
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j) tile.v[j][lane] = v[j][0], tile.v[j][lane + 32] = v[j][1];
+    }
+  }
+  __device__ __forceinline__ void next(long long span) { p += span * token; }
+};
 
 // Rows that are in no sequence leave the state exactly as it is: their gate r
 // becomes -infinity and everything else 0.  Whole warps; `used`: bit j is row j.
@@ -522,7 +540,7 @@ struct ForwardShared {
 };
 
 template <typename T, bool PACKED, bool ALIGNED>
-__global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const ScanArgs a) {
+__global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const __grid_constant__ ScanArgs a) {
   constexpr int STEPS = kForwardSteps, V = 2;
   constexpr unsigned kAll = (1u << STEPS) - 1;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -530,28 +548,28 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const ScanA
   ptx::pdl_wait_prev();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = cluster_rank(), ctas = cluster_size();
-  const int c0 = static_cast<int>(blockIdx.x / ctas) * 64, c = c0 + lane * V, n = blockIdx.y;
+  const int c0 = static_cast<int>(blockIdx.x / ctas) * 64, c = c0 + lane * V, n = blockIdx.y, L = static_cast<int>(a.L);
   // with rows that are not aligned C may be odd: the last channel stands alone
-  const int width = min(V, a.C - c);
+  const int width = min(V, a.C - c), there = a.C - c0;
   const bool in = width > 0;
   auto& tile = sh.warp[warp];
-  T* y = static_cast<T*>(a.y) + (n * a.L) * a.C + c;
-  const long long blocks = (a.L + GATED_SCAN_STATE_EVERY - 1) / GATED_SCAN_STATE_EVERY;
   const Vf<V> decay = scan_initial<V>(a.decay, 0, a.C, c, width);
   Vf<V> carry = PACKED ? splat<V>(0.f) : scan_initial<V>(a.h0, n, a.C, c, width);
   if (PACKED) pass_empty<V>(a, a.h0, a.h_last, rank * kScanWarps + warp, ctas * kScanWarps, c, width);
   if (ctas > 1) cluster_arrive(false), cluster_wait();  // every CTA runs before another writes to its shared memory
-  const long long span = static_cast<long long>(ctas) * kScanWarps * STEPS;
+  const int span = ctas * kScanWarps * STEPS;
   const int turns = static_cast<int>((a.L + span - 1) / span);
-  long long t0 = (rank * kScanWarps + warp) * STEPS;
-  const auto load = [&](long long t) {
-    load_tile<T, STEPS, ALIGNED>(tile.r, a.r, n, a.L, a.C, t, c0);
-    load_tile<T, STEPS, ALIGNED>(tile.i, a.i, n, a.L, a.C, t, c0);
-    load_tile<T, STEPS, ALIGNED>(tile.x, a.x, n, a.L, a.C, t, c0);
-  };
-  load(t0);
-  for (int turn = 0; turn < turns; ++turn, t0 += span) {
-    const ScanTokens tok = scan_tokens<STEPS, PACKED>(a, t0);
+  int left = L - (rank * kScanWarps + warp) * STEPS;  // rows from the warp's first of this turn to the end
+  TileWalk<T, STEPS, ALIGNED> x, r, i;
+  r.start(a.r, n, L - left, c0);
+  i.start(a.i, n, L - left, c0);
+  x.start(a.x, n, L - left, c0);
+  r.load(tile.r, left, there);
+  i.load(tile.i, left, there);
+  x.load(tile.x, left, there);
+  T* y = static_cast<T*>(a.y) + (n * a.L + L - left) * a.C + c;
+  for (int turn = 0; turn < turns; ++turn, left -= span, y += static_cast<long long>(span) * a.C) {
+    const ScanTokens tok = scan_tokens<STEPS, PACKED>(a, L - left);
     copies_done();
     if (tok.used != kAll) {
       void_rows(tile.r, tok.used, -INFINITY);
@@ -565,32 +583,44 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const ScanA
     for (int j = 0; j < STEPS; ++j) {
       const GateValues<V> g = gate_values<V>(a.consts, gate_input<T, V>(row_pair(tile.r, j, lane)),
                                              gate_input<T, V>(row_pair(tile.i, j, lane)), decay);
-      Vf<V> x;
-      unpack<T, V>(row_pair(tile.x, j, lane), x.v);
-      u[j] = gated_input<V>(g, g.m, x);
+      Vf<V> xv;
+      unpack<T, V>(row_pair(tile.x, j, lane), xv.v);
+      u[j] = gated_input<V>(g, g.m, xv);
       av[j] = g.a;
       if (PACKED && (tok.first >> j & 1))
         mine = ScanMap<V>{splat<V>(-1.f), scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, width)};
       then_token<PACKED>(mine, av[j], u[j]);
     }
     __syncwarp();
-    Vf<V> h = scan_exchange<PACKED, V>(sh.maps, turn & 1, warp, rank, ctas, mine, carry, [&] { load(t0 + span); });
-    if (in && a.states && t0 < a.L && t0 % GATED_SCAN_STATE_EVERY == 0)
-      put_state<V>(a.states, n * blocks + t0 / GATED_SCAN_STATE_EVERY, a.C, c, width, h);
-    T* out = y + t0 * a.C;
+    const auto load = [&] {
+      r.next(span);
+      i.next(span);
+      x.next(span);
+      r.load(tile.r, left - span, there);
+      i.load(tile.i, left - span, there);
+      x.load(tile.x, left - span, there);
+    };
+    Vf<V> h = scan_exchange<PACKED, V>(sh.maps, turn & 1, warp, rank, ctas, mine, carry, [&] {
+      if constexpr (ALIGNED) load();
+    });
+    if (in && a.states && left > 0 && (L - left) % GATED_SCAN_STATE_EVERY == 0)
+      put_state<V>(a.states,
+                   n * ((a.L + GATED_SCAN_STATE_EVERY - 1) / GATED_SCAN_STATE_EVERY) + (L - left) / GATED_SCAN_STATE_EVERY,
+                   a.C, c, width, h);
+    T* out = y;
 #pragma unroll
-    for (int j = 0; j < STEPS; ++j) {
+    for (int j = 0; j < STEPS; ++j, out += a.C) {
       if (PACKED && (tok.first >> j & 1))
         h = scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, width);
       h = fma_v(av[j], h, u[j]);
-      if (in && (tok.used >> j & 1)) put_row<T, V, ALIGNED>(out + static_cast<long long>(j) * a.C, width, h);
-      else if (PACKED && in && a.fill && t0 + j < a.L)
-        put_row<T, V, ALIGNED>(out + static_cast<long long>(j) * a.C, width, splat<V>(0.f));
+      if (in && (tok.used >> j & 1)) put_row<T, V, ALIGNED>(out, width, h);
+      else if (PACKED && in && a.fill && j < left) put_row<T, V, ALIGNED>(out, width, splat<V>(0.f));
       if (PACKED && (tok.last >> j & 1)) {
         const int s = __shfl_sync(0xffffffffu, tok.seq, j);
         if (in && a.h_last) put_state<V>(a.h_last, s, a.C, c, width, h);
       }
     }
+    if constexpr (!ALIGNED) load();
   }
   copies_done();
   if (!PACKED && in && a.h_last && rank == 0 && warp == 0) put_state<V>(a.h_last, n, a.C, c, width, carry);
