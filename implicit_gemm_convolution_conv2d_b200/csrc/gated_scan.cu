@@ -38,11 +38,6 @@ bool rows_take16(const ScanIn& in, bool packed, int esize) {
   return rows_aligned(in.p, packed ? 0 : in.batch, in.token, in.scale ? 1 : esize, 16);
 }
 
-bool rows_take(const ScanIn& in, bool packed, int esize, int V) {
-  const int es = in.scale ? 1 : esize;
-  return rows_aligned(in.p, packed ? 0 : in.batch, in.token, es, static_cast<size_t>(es) * V);
-}
-
 template <typename T, bool PACKED, bool ALIGNED>
 cudaError_t forward_as(const ScanArgs& a, cudaStream_t st) {
   const int s = cluster_of(a.N, a.L, a.C, PACKED, kScanWarps * kForwardSteps);
@@ -62,30 +57,32 @@ cudaError_t launch_forward(const ScanArgs& a, cudaStream_t st) {
   return p ? forward_as<T, true, false>(a, st) : forward_as<T, false, false>(a, st);
 }
 
-template <typename T, int V, bool PACKED, bool Q8>
+// `parts`: the partial sums of ddecay.
+template <typename T, bool PACKED, bool ALIGNED, bool Q8>
 cudaError_t grad_as(const ScanArgs& a, int& parts, cudaStream_t st) {
   const int s = cluster_of(a.N, a.L, a.C, PACKED, GATED_SCAN_STATE_EVERY);
-  const dim3 grid((a.C + 32 * V - 1) / (32 * V) * s, PACKED ? 1 : a.N);
+  const dim3 grid((a.C + 63) / 64 * s, PACKED ? 1 : a.N);
   parts = s * static_cast<int>(grid.y);
-  return launch_pdl(gated_scan_grad_kernel<T, V, PACKED, Q8>, grid, dim3(kScanThreads), 0, st, s, a);
+  auto* k = gated_scan_grad_kernel<T, PACKED, ALIGNED, Q8>;
+  const size_t smem = sizeof(GradShared<T>);
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  return e != cudaSuccess ? e : launch_pdl(k, grid, dim3(kScanThreads), smem, st, s, a);
 }
 
-template <typename T, int V>
+template <typename T, bool PACKED>
 cudaError_t grad_by(const ScanArgs& a, int& parts, cudaStream_t st) {
-  if (a.x.scale || a.r.scale || a.i.scale)
-    return a.packed ? grad_as<T, V, true, true>(a, parts, st) : grad_as<T, V, false, true>(a, parts, st);
-  return a.packed ? grad_as<T, V, true, false>(a, parts, st) : grad_as<T, V, false, false>(a, parts, st);
+  bool aligned = a.C % (16 / static_cast<int>(sizeof(T))) == 0;
+  for (const ScanIn* in : {&a.x, &a.r, &a.i, &a.dy})
+    aligned = aligned && (!in->scale || a.C % 16 == 0) && rows_take16(*in, PACKED, sizeof(T));
+  for (const void* out : {a.dx, a.dr, a.di}) aligned = aligned && aligned_to(out, 2 * sizeof(T));
+  if (a.x.scale)
+    return aligned ? grad_as<T, PACKED, true, true>(a, parts, st) : grad_as<T, PACKED, false, true>(a, parts, st);
+  return aligned ? grad_as<T, PACKED, true, false>(a, parts, st) : grad_as<T, PACKED, false, false>(a, parts, st);
 }
 
-// `parts`: the partial sums of ddecay.
 template <typename T>
 cudaError_t launch_grad(const ScanArgs& a, int& parts, cudaStream_t st) {
-  constexpr int kV = 2;
-  const bool p = a.packed;
-  bool vec = a.C % kV == 0;
-  for (const ScanIn* in : {&a.x, &a.r, &a.i, &a.dy}) vec = vec && rows_take(*in, p, sizeof(T), kV);
-  for (const void* out : {a.dx, a.dr, a.di}) vec = vec && aligned_to(out, sizeof(T) * kV);
-  return vec ? grad_by<T, kV>(a, parts, st) : grad_by<T, 1>(a, parts, st);
+  return a.packed ? grad_by<T, true>(a, parts, st) : grad_by<T, false>(a, parts, st);
 }
 
 template <typename T>
@@ -179,6 +176,11 @@ int gated_scan_grad(const void* x, const unsigned char* x_scale, const void* r, 
   if (rc == CONV_OK) rc = take_input(a.i, ins + 4, i, i_scale, i_batch, i_token, N, L, C, packed, es);
   if (rc == CONV_OK) rc = take_input(a.dy, ins + 6, dy, nullptr, dy_batch, dy_token, N, L, C, packed, es);
   if (rc != CONV_OK) return rc;
+  if ((x_scale == nullptr) != (r_scale == nullptr) || (x_scale == nullptr) != (i_scale == nullptr))
+    return CONV_EUNSUPPORTED;
+  if (x_scale)  // checkpoints are contiguous
+    for (const ScanIn* in : {&a.x, &a.r, &a.i})
+      if ((L > 1 && in->token != C) || (!packed && N > 1 && in->batch != L * C)) return CONV_EUNSUPPORTED;
   const long long rows = packed ? L : N * L, nc = static_cast<long long>(N) * C;
   if (!decay || !ddecay || (rows > 0 && (!dx || !dr || !di || !states))) return CONV_EINVAL;
   unsigned long long need = 0;

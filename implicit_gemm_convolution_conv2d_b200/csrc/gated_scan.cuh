@@ -218,77 +218,7 @@ __device__ __forceinline__ void then_token(ScanMap<V>& f, const Vf<V>& a, const 
   for (int k = 0; k < V; ++k) f.P[k] = PACKED && f.P[k] < 0.f ? -1.f : P[k];
 }
 
-// V channels of kScanSteps rows of an input, loaded together: rows t0 + j for
-// the bits j of `used`.  The others are 0, or with GATE -infinity: a row whose
-// gate r is that, and whose x is 0, leaves the state exactly as it is.
 constexpr unsigned kScanAll = (1u << kScanSteps) - 1;
-
-template <typename T, int V, bool Q8, bool GATE>
-struct ScanRows {
-  using R = Raw<T, V>;
-  using R8 = typename RawVec<V>::type;
-  R raw[kScanSteps];
-  unsigned char byte[Q8 ? kScanSteps : 1];
-
-  __device__ __forceinline__ void load(const ScanIn& in, int n, long long L, int C, long long t0, int c, unsigned used) {
-    if (Q8 && in.scale) {
-      const signed char* p = static_cast<const signed char*>(in.p) + n * in.batch + t0 * in.token + c;
-      const int nblk = (C + ACT8_BLOCK - 1) / ACT8_BLOCK;
-      const unsigned char* sc = in.scale + (n * L + t0) * nblk + c / ACT8_BLOCK;
-#pragma unroll
-      for (int j = 0; j < kScanSteps; ++j) {
-        union {
-          R r;
-          R8 q;
-          signed char e[V];
-        } u;
-        u.r = R();
-#pragma unroll
-        for (int k = 0; k < V; ++k) u.e[k] = GATE ? -128 : 0;
-        byte[Q8 ? j : 0] = 254;  // -128 * 2^127
-        if (used >> j & 1) {
-          u.q = __ldg(reinterpret_cast<const R8*>(p + j * in.token));
-          byte[Q8 ? j : 0] = __ldg(sc + j * nblk);
-        }
-        raw[j] = u.r;
-      }
-      return;
-    }
-    const T* p = static_cast<const T*>(in.p) + n * in.batch + t0 * in.token + c;
-    if (used == kScanAll) {
-#pragma unroll
-      for (int j = 0; j < kScanSteps; ++j) raw[j] = load_raw<T, V>(p + j * in.token);
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < kScanSteps; ++j) {
-      union {
-        R r;
-        T e[V];
-      } u;
-#pragma unroll
-      for (int k = 0; k < V; ++k) u.e[k] = from_f32<T>(GATE ? -INFINITY : 0.f);
-      raw[j] = u.r;
-      if (used >> j & 1) raw[j] = load_raw<T, V>(p + j * in.token);
-    }
-  }
-  __device__ __forceinline__ Vf<V> get(int j, const ScanIn& in) const {
-    Vf<V> o;
-    if (Q8 && in.scale) {
-      union {
-        R r;
-        signed char e[V];
-      } u;
-      u.r = raw[j];
-      const float step = act8_step(byte[Q8 ? j : 0]);
-#pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = static_cast<float>(u.e[k]) * step;
-    } else {
-      unpack<T, V>(raw[j], o.v);
-    }
-    return o;
-  }
-};
 
 // What the tokens t0 .. t0 + STEPS - 1 are: bit j of `used` where token
 // t0 + j is in a sequence, of `first` and `last` where it begins or ends one;
@@ -502,8 +432,8 @@ struct TileWalk {
       const T* from = p + lane;
 #pragma unroll
       for (int j = 0; j < STEPS; ++j) {
-        v[j][0] = j < rows && lane < width ? from[0] : from_f32<T>(0.f);
-        v[j][1] = j < rows && lane + 32 < width ? from[32] : from_f32<T>(0.f);
+        v[j][0] = j < rows && lane < width ? from[0] : T(0.f);
+        v[j][1] = j < rows && lane + 32 < width ? from[32] : T(0.f);
         from += token;
       }
 #pragma unroll
@@ -516,10 +446,10 @@ struct TileWalk {
 // Rows that are in no sequence leave the state exactly as it is: their gate r
 // becomes -infinity and everything else 0.  Whole warps; `used`: bit j is row j.
 template <typename T, int STEPS>
-__device__ __forceinline__ void void_rows(ScanTile<T, STEPS>& tile, unsigned used, float with) {
+__device__ __forceinline__ void void_rows(ScanTile<T, STEPS>& tile, unsigned used, T with) {
   const int lane = threadIdx.x & 31;
   for (int j = 0; j < STEPS; ++j)
-    if (!(used >> j & 1)) tile.v[j][lane] = tile.v[j][lane + 32] = from_f32<T>(with);
+    if (!(used >> j & 1)) tile.v[j][lane] = tile.v[j][lane + 32] = with;
 }
 
 template <typename T, int STEPS>
@@ -572,9 +502,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const __gri
     const ScanTokens tok = scan_tokens<STEPS, PACKED>(a, L - left);
     copies_done();
     if (tok.used != kAll) {
-      void_rows(tile.r, tok.used, -INFINITY);
-      void_rows(tile.i, tok.used, 0.f);
-      void_rows(tile.x, tok.used, 0.f);
+      void_rows(tile.r, tok.used, from_f32<T>(-INFINITY));
+      void_rows(tile.i, tok.used, from_f32<T>(0.f));
+      void_rows(tile.x, tok.used, from_f32<T>(0.f));
       __syncwarp();
     }
     Vf<V> av[STEPS], u[STEPS];
@@ -626,130 +556,253 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const __gri
   if (!PACKED && in && a.h_last && rank == 0 && warp == 0) put_state<V>(a.h_last, n, a.C, c, width, carry);
 }
 
-template <typename T, int V, bool PACKED, bool Q8>
-__global__ void __launch_bounds__(kScanThreads, 2) gated_scan_grad_kernel(const ScanArgs a) {
-  __shared__ ScanShared<V> sh;
-  __shared__ ScanMap<V> ahead[2][kScanWarps][32];
+// ---- the backward pass -----------------------------------------------------
+
+// x, r and i of the backward pass on their way to the tiles: elements with
+// strides of their own, or with Q8 checkpoints' bytes, which each warp expands in
+// place once they are there (they are exact in T): 16 a lane, of one row and one
+// block of 32, whose step's byte the lane has loaded with them.
+template <typename T, bool Q8, bool ALIGNED>
+struct GradRows {
+  TileWalk<T, kScanSteps, ALIGNED> x, r, i;
+  __device__ __forceinline__ void start(const ScanArgs& a, int n, long long t0, int c0) {
+    x.start(a.x, n, t0, c0);
+    r.start(a.r, n, t0, c0);
+    i.start(a.i, n, t0, c0);
+  }
+  template <typename Tiles>
+  __device__ __forceinline__ void load(const ScanArgs&, Tiles& to, int rows, int width) {
+    r.load(to.r, rows, width);
+    i.load(to.i, rows, width);
+    x.load(to.x, rows, width);
+  }
+  __device__ __forceinline__ void next(const ScanArgs&, long long span) {
+    x.next(span);
+    r.next(span);
+    i.next(span);
+  }
+  template <typename Tiles>
+  __device__ __forceinline__ void expand(Tiles&) const {}
+};
+
+template <typename T, bool ALIGNED>
+struct GradRows<T, true, ALIGNED> {
+  using Tile = ScanTile<T, kScanSteps>;
+  using Tile8 = ScanTile<signed char, kScanSteps>;
+  static_assert(kScanSteps * 64 == 32 * 16, "16 bytes a lane");
+  long long at, block;  // the walk's first element and the lane's step: the three are laid out alike
+  int xs, rs, is;       // the lane's steps' bytes
+
+  __device__ __forceinline__ void start(const ScanArgs& a, int n, long long t0, int c0) {
+    const int lane = threadIdx.x & 31;
+    at = (n * a.L + t0) * a.C + c0;
+    block = (n * a.L + t0 + lane / 4) * ((a.C + ACT8_BLOCK - 1) / ACT8_BLOCK) + c0 / ACT8_BLOCK + lane % 4 / 2;
+  }
+  __device__ __forceinline__ int load_one(const ScanArgs& a, const ScanIn& in, Tile& tile, int rows, int width) const {
+    const int lane = threadIdx.x & 31;
+    TileWalk<signed char, kScanSteps, ALIGNED> walk;
+    walk.start(ScanIn{static_cast<const signed char*>(in.p) + at, nullptr, 0, a.C}, 0, 0, 0);
+    walk.load(reinterpret_cast<Tile8&>(tile), rows, width);
+    return lane / 4 < rows && lane % 4 / 2 * ACT8_BLOCK < width ? __ldg(in.scale + block) : 0;
+  }
+  template <typename Tiles>
+  __device__ __forceinline__ void load(const ScanArgs& a, Tiles& to, int rows, int width) {
+    rs = load_one(a, a.r, to.r, rows, width);
+    is = load_one(a, a.i, to.i, rows, width);
+    xs = load_one(a, a.x, to.x, rows, width);
+  }
+  __device__ __forceinline__ void next(const ScanArgs& a, long long span) {
+    at += span * a.C;
+    block += span * ((a.C + ACT8_BLOCK - 1) / ACT8_BLOCK);
+  }
+  static __device__ __forceinline__ void expand_one(Tile& tile, int byte) {
+    const int lane = threadIdx.x & 31;
+    const uint4 raw = reinterpret_cast<const uint4*>(&tile)[lane];
+    const float step = act8_step(static_cast<unsigned char>(byte));
+    __syncwarp();
+    T* to = &tile.v[lane / 4][lane % 4 * 16];
+    const unsigned words[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      // q + 128 as the last byte of 2^23: a conversion would take the special functions' pipe
+      const unsigned biased = words[q] ^ 0x80808080u;
+      Vf<4> v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7650 + k));
+      v = mul_v(add_v(v, splat<4>(-8388736.f)), splat<4>(step));
+      store_vec<T, 4>(to + 4 * q, v.v);
+    }
+  }
+  template <typename Tiles>
+  __device__ __forceinline__ void expand(Tiles& t) const {
+    expand_one(t.r, rs);
+    expand_one(t.i, is);
+    expand_one(t.x, xs);
+    __syncwarp();
+  }
+};
+
+template <typename T>
+struct GradShared {
+  ScanShared<2> maps;
+  ScanMap<2> ahead[2][kScanWarps][32];  // the forward maps, within the CTA
+  struct {
+    ScanTile<T, kScanSteps> x, dy;
+    union {
+      struct {
+        ScanTile<T, kScanSteps> r, i;
+      };
+      float2 m[kScanSteps][32];  // m, once r and i are used
+    };
+  } tile[kScanWarps][2];  // the turn at hand and the next
+  float2 s[kScanWarps][kScanSteps][32];
+};
+
+template <typename T, bool PACKED, bool ALIGNED, bool Q8>
+__global__ void __launch_bounds__(kScanThreads, 2) gated_scan_grad_kernel(const __grid_constant__ ScanArgs a) {
+  constexpr int STEPS = kScanSteps, V = 2;
+  extern __shared__ __align__(128) unsigned char smem[];
+  GradShared<T>& sh = *reinterpret_cast<GradShared<T>*>(smem);
   ptx::pdl_wait_prev();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = cluster_rank(), ctas = cluster_size();
-  const int c = (static_cast<int>(blockIdx.x / ctas) * 32 + lane) * V, n = blockIdx.y;
-  const bool in = c < a.C;
+  const int c0 = static_cast<int>(blockIdx.x / ctas) * 64, c = c0 + lane * V, n = blockIdx.y;
+  const int width = min(V, a.C - c), there = a.C - c0;
+  const bool in = width > 0;
   const long long blocks = (a.L + GATED_SCAN_STATE_EVERY - 1) / GATED_SCAN_STATE_EVERY;
-  Vf<V> decay, dd = splat<V>(0.f);
-#pragma unroll
-  for (int k = 0; k < V; ++k) decay[k] = in ? __ldg(a.decay + c + k) : 0.f;
-  Vf<V> carry = PACKED ? splat<V>(0.f) : scan_initial<V>(a.dh_last, n, a.C, c, in * V);
-  if (PACKED) pass_empty<V>(a, a.dh_last, a.dh0, rank * kScanWarps + warp, ctas * kScanWarps, c, in * V);
+  const Vf<V> decay = scan_initial<V>(a.decay, 0, a.C, c, width);
+  Vf<V> carry = PACKED ? splat<V>(0.f) : scan_initial<V>(a.dh_last, n, a.C, c, width), dd = splat<V>(0.f);
+  if (PACKED) pass_empty<V>(a, a.dh_last, a.dh0, rank * kScanWarps + warp, ctas * kScanWarps, c, width);
   if (ctas > 1) cluster_arrive(false), cluster_wait();  // every CTA runs before another writes to its shared memory
-  const long long span = static_cast<long long>(ctas) * GATED_SCAN_STATE_EVERY;
+  const int span = ctas * GATED_SCAN_STATE_EVERY;
   const int turns = static_cast<int>((a.L + span - 1) / span);
-  for (int turn = turns - 1; turn >= 0; --turn) {
-    const long long block = turn * static_cast<long long>(ctas) + rank, begin = block * GATED_SCAN_STATE_EVERY;
-    const long long t0 = begin + warp * kScanSteps;
-    const ScanTokens tok = scan_tokens<kScanSteps, PACKED>(a, t0);
-    const unsigned used = in ? tok.used : 0;
-    ScanRows<T, V, Q8, false> x, i;
-    ScanRows<T, V, Q8, true> r;
-    ScanRows<T, V, false, false> dy;
-    r.load(a.r, n, a.L, a.C, t0, c, used);
-    i.load(a.i, n, a.L, a.C, t0, c, used);
-    x.load(a.x, n, a.L, a.C, t0, c, used);
-    dy.load(a.dy, n, a.L, a.C, t0, c, used);
+  // from the last turn to the first; t0: the warp's first row
+  long long t0 = (turns - 1) * static_cast<long long>(span) + rank * GATED_SCAN_STATE_EVERY + warp * STEPS;
+  GradRows<T, Q8, ALIGNED> in3;
+  TileWalk<T, STEPS, ALIGNED> dy;
+  in3.start(a, n, t0, c0);
+  dy.start(a.dy, n, t0, c0);
+  const auto load = [&](auto& tile, long long t) {
+    const int rows = t < 0 ? 0 : static_cast<int>(min(a.L - t, static_cast<long long>(STEPS)));
+    in3.load(a, tile, rows, there);
+    dy.load(tile.dy, rows, there);
+  };
+  if (turns > 0) load(sh.tile[warp][(turns - 1) & 1], t0);
+  long long row = (n * a.L + t0) * a.C + c;
+  for (int turn = turns - 1; turn >= 0; --turn, t0 -= span, row -= static_cast<long long>(span) * a.C) {
+    const long long block = t0 / GATED_SCAN_STATE_EVERY;
+    const int b = turn & 1;
+    auto& tile = sh.tile[warp][b];
+    const ScanTokens tok = scan_tokens<STEPS, PACKED>(a, t0);
     // the state in front of the CTA's tokens
-    const bool start = !PACKED && begin == 0;
-    Vf<V> h = scan_initial<V>(start ? a.h0 : a.states_in, start ? n : n * blocks + block, a.C, c, in && begin < a.L ? V : 0);
-    Vf<V> av[kScanSteps], s[kScanSteps], g[kScanSteps], m2[kScanSteps];  // m2 = 1 - a^2
+    const bool start = !PACKED && block == 0;
+    Vf<V> h = scan_initial<V>(start ? a.h0 : a.states_in, start ? n : n * blocks + block, a.C, c, block < blocks ? width : 0);
+    copies_done();
+    in3.expand(tile);
+    if (tok.used != kScanAll) {
+      void_rows(tile.r, tok.used, from_f32<T>(-INFINITY));
+      void_rows(tile.i, tok.used, from_f32<T>(0.f));
+      void_rows(tile.x, tok.used, from_f32<T>(0.f));
+      void_rows(tile.dy, tok.used, from_f32<T>(0.f));
+      __syncwarp();
+    }
+    const auto row_of = [&](const auto& t, int j) {
+      Vf<V> v;
+      unpack<T, V>(row_pair(t, j, lane), v.v);
+      return v;
+    };
+    Vf<V> av[STEPS], g[STEPS], over[STEPS];  // over: 1 / m, 0 where a = 1; s and m go to shared memory
+    Vf<V> mv[STEPS];
     ScanMap<V> fwd = no_map<V>(), bwd = no_map<V>();
 #pragma unroll
-    for (int j = 0; j < kScanSteps; ++j) {
-      const GateValues<V> gv = gate_values<V, false>(a.consts, lowest(r.get(j, a.r)), lowest(i.get(j, a.i)), decay);
-      s[j] = gv.s;
+    for (int j = 0; j < STEPS; ++j) {
+      const GateValues<V> gv = gate_values<V, false>(a.consts, gate_input<T, V>(row_pair(tile.r, j, lane)),
+                                                     gate_input<T, V>(row_pair(tile.i, j, lane)), decay);
+#pragma unroll
+      for (int k = 0; k < V; ++k) over[j][k] = gv.m[k] > 0.f ? rsqrt_approx(gv.m[k]) : gv.m[k];
+      mv[j] = mul_v(gv.m, over[j]);
+      const Vf<V> sv = fma_v(gv.nan, splat<V>(0.f), gv.s);  // NaN where a gate is
+      sh.s[warp][j][lane] = make_float2(sv[0], sv[1]);
       g[j] = gv.g;
-      m2[j] = gv.m;
       av[j] = gv.a;
-      Vf<V> m;
-#pragma unroll
-      for (int k = 0; k < V; ++k) m[k] = sqrt_approx(m2[j][k]);
       if (PACKED && (tok.first >> j & 1))
-        fwd = ScanMap<V>{splat<V>(-1.f), scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, in * V)};
-      then_token<PACKED>(fwd, av[j], gated_input<V>(gv, m, x.get(j, a.x)));
+        fwd = ScanMap<V>{splat<V>(-1.f), scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, width)};
+      then_token<PACKED>(fwd, av[j], gated_input<V>(gv, mv[j], row_of(tile.x, j)));
     }
+    __syncwarp();
 #pragma unroll
-    for (int j = kScanSteps - 1; j >= 0; --j) {
+    for (int j = 0; j < STEPS; ++j) tile.m[j][lane] = make_float2(mv[j][0], mv[j][1]);
+#pragma unroll
+    for (int j = STEPS - 1; j >= 0; --j) {
       if (PACKED && (tok.last >> j & 1))
-        bwd = ScanMap<V>{splat<V>(-1.f), scan_initial<V>(a.dh_last, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, in * V)};
-      then_token<PACKED>(bwd, av[j], mul_v(av[j], dy.get(j, a.dy)));
+        bwd = ScanMap<V>{splat<V>(-1.f), scan_initial<V>(a.dh_last, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, width)};
+      then_token<PACKED>(bwd, av[j], mul_v(av[j], row_of(tile.dy, j)));
     }
     // forward only within the CTA, whose first state is kept; backward through
     // the cluster, whose last warp comes first (the barriers inside cover both)
-    const int b = turn & 1;
-    ahead[b][warp][lane] = fwd;
-    Vf<V> G = scan_exchange<PACKED, V>(sh, b, kScanWarps - 1 - warp, ctas - 1 - rank, ctas, bwd, carry, [] {});
+    sh.ahead[b][warp][lane] = fwd;
+    Vf<V> G = scan_exchange<PACKED, V>(sh.maps, b, kScanWarps - 1 - warp, ctas - 1 - rank, ctas, bwd, carry, [&] {
+      in3.next(a, -span);
+      dy.next(-span);
+      load(sh.tile[warp][b ^ 1], t0 - span);
+    });
 #pragma unroll
     for (int w = 0; w < kScanWarps - 1; ++w)
-      if (w < warp) h = follow<PACKED>(ahead[b][w][lane], h);
-    Vf<V> hp[kScanSteps];  // the state in front of each token
+      if (w < warp) h = follow<PACKED>(sh.ahead[b][w][lane], h);
+    const auto pair_of = [](const float2& v) { return Vf<V>{{v.x, v.y}}; };
+    Vf<V> hp[STEPS];  // the state in front of each token
 #pragma unroll
-    for (int j = 0; j < kScanSteps; ++j) {
+    for (int j = 0; j < STEPS; ++j) {
       if (PACKED && (tok.first >> j & 1))
-        h = scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, in * V);
+        h = scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, width);
       hp[j] = h;
-      Vf<V> m;
-#pragma unroll
-      for (int k = 0; k < V; ++k) m[k] = sqrt_approx(m2[j][k]);
-      h = fma_v(av[j], h, mul_v(mul_v(m, g[j]), x.get(j, a.x)));
+      h = fma_v(av[j], h, mul_v(mul_v(pair_of(tile.m[j][lane]), g[j]), row_of(tile.x, j)));
     }
-    const long long row = (n * a.L + t0) * a.C + c;
     Vf<V> part = splat<V>(0.f);
 #pragma unroll
-    for (int j = kScanSteps - 1; j >= 0; --j) {
+    for (int j = STEPS - 1; j >= 0; --j) {
       if (PACKED && (tok.last >> j & 1))
-        G = scan_initial<V>(a.dh_last, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, in * V);
-      const Vf<V> xv = x.get(j, a.x), one = splat<V>(1.f);
-      Vf<V> over;  // 1 / m, 0 where a = 1
-#pragma unroll
-      for (int k = 0; k < V; ++k) over[k] = m2[j][k] > 0.f ? rsqrt_approx(m2[j][k]) : m2[j][k];
-      const Vf<V> m = mul_v(m2[j], over);
-      const Vf<V> whole = add_v(dy.get(j, a.dy), G), vx = mul_v(g[j], xv), Gm = mul_v(whole, m);
+        G = scan_initial<V>(a.dh_last, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, width);
+      const Vf<V> one = both<V>(a.consts.one), none1 = both<V>(a.consts.none);
+      const Vf<V> whole = add_v(row_of(tile.dy, j), G), vx = mul_v(g[j], row_of(tile.x, j));
+      const Vf<V> Gm = mul_v(whole, pair_of(tile.m[j][lane]));
       G = mul_v(av[j], whole);
-      const Vf<V> back = mul_v(mul_v(av[j], vx), over);
-      const Vf<V> dl = mul_v(G, add_v(hp[j], neg_v(back))), sdl = mul_v(s[j], dl);
-      const Vf<V> dx = mul_v(Gm, g[j]), di = mul_v(mul_v(Gm, vx), fma_v(g[j], splat<V>(-1.f), one));
-      const Vf<V> dr = mul_v(mul_v(neg_v(decay), sdl), fma_v(s[j], splat<V>(-1.f), one));
+      const Vf<V> back = mul_v(mul_v(av[j], vx), over[j]);
+      const Vf<V> sv = pair_of(sh.s[warp][j][lane]);
+      const Vf<V> dl = mul_v(G, fma_v(back, none1, hp[j])), sdl = mul_v(sv, dl);
+      const Vf<V> dx = mul_v(Gm, g[j]), di = mul_v(mul_v(Gm, vx), fma_v(g[j], none1, one));
+      const Vf<V> dr = mul_v(mul_v(neg_v(decay), sdl), fma_v(sv, none1, one));
       const long long at = row + static_cast<long long>(j) * a.C;
-      if (used >> j & 1) {
+      if (in && (tok.used >> j & 1)) {
         part = add_v(part, sdl);
-        store_vec<T, V>(static_cast<T*>(a.dx) + at, dx.v);
-        store_vec<T, V>(static_cast<T*>(a.dr) + at, dr.v);
-        store_vec<T, V>(static_cast<T*>(a.di) + at, di.v);
+        put_row<T, V, ALIGNED>(static_cast<T*>(a.dx) + at, width, dx);
+        put_row<T, V, ALIGNED>(static_cast<T*>(a.dr) + at, width, dr);
+        put_row<T, V, ALIGNED>(static_cast<T*>(a.di) + at, width, di);
       } else if (PACKED && in && a.fill && t0 + j < a.L) {
-        store_zero<T, V>(static_cast<T*>(a.dx) + at);
-        store_zero<T, V>(static_cast<T*>(a.dr) + at);
-        store_zero<T, V>(static_cast<T*>(a.di) + at);
+        put_row<T, V, ALIGNED>(static_cast<T*>(a.dx) + at, width, splat<V>(0.f));
+        put_row<T, V, ALIGNED>(static_cast<T*>(a.dr) + at, width, splat<V>(0.f));
+        put_row<T, V, ALIGNED>(static_cast<T*>(a.di) + at, width, splat<V>(0.f));
       }
       if (PACKED && (tok.first >> j & 1)) {
         const int q = __shfl_sync(0xffffffffu, tok.seq, j);
-        if (in && a.dh0) put_state<V>(a.dh0, q, a.C, c, V, G);
+        if (in && a.dh0) put_state<V>(a.dh0, q, a.C, c, width, G);
       }
     }
     dd = add_v(dd, part);
+    __syncwarp();
   }
-  if (!PACKED && in && a.dh0 && rank == 0 && warp == 0) put_state<V>(a.dh0, n, a.C, c, V, carry);
+  copies_done();
+  if (!PACKED && in && a.dh0 && rank == 0 && warp == 0) put_state<V>(a.dh0, n, a.C, c, width, carry);
   // ddecay: the CTA's warps in order
   __syncthreads();
-  float* sums = &sh.warp[0][0][0].P[0];
-#pragma unroll
-  for (int k = 0; k < V; ++k) sums[(warp * V + k) * 32 + lane] = dd[k];
+  sh.maps.warp[0][warp][lane].P = dd;
   __syncthreads();
-  if (warp == 0 && in)
+  if (warp == 0 && in) {
+    Vf<V> sum = splat<V>(0.f);
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      float sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kScanWarps; ++w) sum -= sums[(w * V + k) * 32 + lane];
-      a.part[(static_cast<long long>(n) * ctas + rank) * a.C + c + k] = sum;
-    }
+    for (int w = 0; w < kScanWarps; ++w) sum = add_v(sum, sh.maps.warp[0][w][lane].P);
+    put_state<V>(a.part, static_cast<long long>(n) * ctas + rank, a.C, c, width, neg_v(sum));
+  }
 }
 
 // ddecay: the partial sums [n][C] added in order.

@@ -410,8 +410,8 @@ def gated_scan_grad(x, r, i, decay, dy, states, *, h0=None, dh_last=None, cu_seq
     """Gradients of gated_scan: (dx, dr, di, ddecay, dh0) from dy, the gradient of
     y, and `dh_last`, that of the last states (if it matters).
 
-    x, r and i may each be the activation or its checkpoint (Act8); `states` are
-    the forward pass's.  ddecay and dh0 are fp32; dh0 is None without h0."""
+    x, r and i may each be the activation or its checkpoint (Act8; a mixture is
+    unpacked into temporaries); `states` are the forward pass's.  ddecay and dh0 are fp32; dh0 is None without h0."""
     what = "gated_scan_grad"
     xv, xs, dtype = _saved(x, what, "x")
     rv, rs, rd = _saved(r, what, "r")
@@ -425,15 +425,19 @@ def gated_scan_grad(x, r, i, decay, dy, states, *, h0=None, dh_last=None, cu_seq
             raise ValueError(f"{what}: {name} must be {dtype} of shape {tuple(xv.shape)}")
     packed = cu_seqlens is not None
     with _On(xv, stream) as on:
+        if not (xs is None) == (rs is None) == (is_ is None):  # a mixture: the kernel takes all or none in 8 bits
+            xv, rv, iv = (act8_unpack(v) if isinstance(v, Act8) else v for v in (x, r, i))
+            xs = rs = is_ = None
         decay = _decay(decay, C, what)
         states = _optional(states, (1 if packed else N, (L + 63) // 64, C), torch.float32, "states", what)
         h0 = _optional(h0, (N, C), torch.float32, "h0", what)
         dh_last = _optional(dh_last, (N, C), torch.float32, "dh_last", what)
+        if xs is not None:
+            xv, rv, iv, xs, rs, is_ = (t.contiguous() for t in (xv, rv, iv, xs, rs, is_))
         xv, xb, xt = _rows(xv, packed)
         rv, rb, rt = _rows(rv, packed)
         iv, ib, it = _rows(iv, packed)
         dy, yb, yt = _rows(dy, packed)
-        xs, rs, is_ = (None if s is None else s.contiguous() for s in (xs, rs, is_))
         dx, dr, di = (torch.empty(dy.shape, dtype=dtype, device=dy.device) for _ in range(3))
         ddecay = torch.empty(C, dtype=torch.float32, device=dy.device)
         dh0 = None if h0 is None else torch.empty((N, C), dtype=torch.float32, device=dy.device)

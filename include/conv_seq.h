@@ -97,7 +97,8 @@ int gated_scan(const void* x, const void* r, const void* i, const float* decay, 
                conv_stream_t stream);
 
 /* Its gradients.  From dy (with strides), the forward pass's inputs (x, r and i
- * each a tensor or a checkpoint) and its `states`: dx, dr, di (like y), ddecay
+ * all tensors, or all contiguous checkpoints; CONV_EUNSUPPORTED where they are
+ * mixed or strided) and its `states`: dx, dr, di (like y), ddecay
  * [C] and dh0 [N, C] (fp32; dh0 may be NULL).  dh_last (fp32, may be NULL) is
  * the gradient of h_last.  With a = 1 (decay * s = 0) the square root's
  * derivative is taken as 0.  ddecay is summed as dw above is. */
