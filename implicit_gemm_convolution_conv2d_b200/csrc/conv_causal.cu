@@ -35,25 +35,32 @@ bool shape_ok(int N, long long L, int C, int K, bool packed) {
          static_cast<long long>(N) * (K - 1) <= kSeqMaxElems / C;
 }
 
-// Tokens a thread: enough threads for `want` where there are the tokens, and
-// between 4 and `most` tokens each, so that the K - 1 rows each reads again
-// stay few.
-int run_length(long long rows, long long vecs, long long want, int most) {
-  long long run = rows * vecs / std::max<long long>(1, want);
-  run = std::min<long long>(std::max<long long>(run, 4), most);
-  return static_cast<int>((run + 3) / 4 * 4);
+// Tokens a warp: enough warps for `per_sm` an SM of a 148-SM B200 (a fixed
+// number: the order of dw's sum must not depend on the device) where there are
+// the tokens, and between 16 and 256 tokens each, a whole number of tiles; K - 1
+// rows a run are read again.
+int run_length(long long rows, int C, int per_sm) {
+  const long long run = rows * ((C + 63) / 64) / (148LL * per_sm);
+  return static_cast<int>(std::min<long long>(std::max<long long>(run, 16), 256) / 16 * 16);
 }
 
-// The gradients' grid: blocks of 32 channel vectors x 8 runs; few enough that
-// their partial sums stay small, four an SM of a 148-SM B200 (a fixed number,
-// so that the order of a sum never depends on the device).
-constexpr long long kGradBlocks = 4 * 148;
-constexpr int kGradRun = 32;
+int grad_run(int N, long long L, int C, bool packed) { return run_length(packed ? L : N * L, C, 16); }
 
-int grad_blocks_y(int C, int V, long long runs) {
-  const long long bx = ((C + V - 1) / V + kGradLanes - 1) / kGradLanes;
-  const long long by = std::min((runs + kGradRows - 1) / kGradRows, (kGradBlocks + bx - 1) / bx);
-  return static_cast<int>(std::max<long long>(1, by));
+// Blocks along the runs, each with a partial sum of its own.
+long long run_blocks(int N, long long L, int run, bool packed) {
+  const long long runs = (L + run - 1) / run * (packed ? 1 : N);
+  return std::max<long long>(1, (runs + kCausalWarps - 1) / kCausalWarps);
+}
+
+bool aligned_rows(const SeqIn& in, bool packed, int C, int esize) {
+  const int e = in.scale ? 1 : esize;
+  return C % (16 / e) == 0 && rows_aligned(in.p, packed ? 0 : in.batch, in.token, e, 16);
+}
+
+template <typename K>
+cudaError_t launch_rows(K* k, dim3 grid, size_t smem, const CausalArgs& a, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  return e != cudaSuccess ? e : launch_pdl(k, grid, dim3(kCausalThreads), smem, st, 1, a);
 }
 
 // Checks shared by the forward and the backward pass.
@@ -97,38 +104,29 @@ int conv_causal(const void* x, const void* w, const void* bias, const void* stat
   if (any_alias(outs, 2, ins, 6)) return CONV_EALIAS;
   if (rows == 0 && window == 0) return CONV_OK;
   CausalArgs a = {};
-  a.x = x, a.w = w, a.bias = bias, a.state = state, a.cu = cu, a.y = y, a.state_out = window > 0 ? state_out : nullptr;
+  a.x = SeqIn{x, nullptr, x_batch, x_token};
+  a.w = w, a.bias = bias, a.state = state, a.cu = cu, a.y = y, a.state_out = window > 0 ? state_out : nullptr;
   a.N = N, a.C = C, a.K = K, a.silu = activation == CONV_ACT_SILU, a.fill = fill != 0;
-  a.L = L, a.x_batch = x_batch, a.x_token = x_token;
+  a.L = static_cast<int>(L);
+  a.run = run_length(rows, C, 24);
+  a.runs = static_cast<int>((L + a.run - 1) / a.run);
+  const long long by = run_blocks(N, L, a.run, packed);
+  if (by > 65535) return CONV_EUNSUPPORTED;
+  const dim3 grid((C + 63) / 64, static_cast<unsigned>(by));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  bool fits = true;
   const cudaError_t e = by_type_and_taps(dtype, K, [&](auto t, auto kt) {
     using T = typename decltype(t)::type;
     constexpr int KT = decltype(kt)::value;
-    // 16 bytes of channels a thread, half of that where eight taps of them would not fit in the registers
-    constexpr int V = (KT == 8 ? 8 : 16) / static_cast<int>(sizeof(T));
-    const size_t bytes = V * sizeof(T);
-    const bool vec = C % V == 0 && rows_aligned(x, packed ? 0 : x_batch, x_token, es, bytes) && aligned_to(y, bytes) &&
-                     aligned_to(state, bytes) && aligned_to(state_out, bytes);
-    const long long vecs = vec ? C / V : C;
-    a.run = run_length(rows, vecs, 148LL * 1024, 32);
-    a.runs = (L + a.run - 1) / a.run;
-    const long long threads = std::max<long long>(1, a.runs * (packed ? 1 : N)) * vecs;
-    const long long blocks = (threads + kCausalThreads - 1) / kCausalThreads;
-    fits = blocks <= 0x7fffffffLL;
-    if (!fits) return cudaSuccess;
-    return launch_pdl(vec ? conv_causal_kernel<T, KT, V> : conv_causal_kernel<T, KT, 1>,
-                      dim3(static_cast<unsigned>(blocks)), dim3(kCausalThreads), 0, st, 1, a);
+    const bool aligned = aligned_rows(a.x, packed, C, es) && aligned_to(y, 2 * es) && aligned_to(state_out, 2 * es);
+    return launch_rows(aligned ? conv_causal_kernel<T, KT, true> : conv_causal_kernel<T, KT, false>, grid,
+                       sizeof(CausalShared<T>), a, st);
   });
-  if (!fits) return CONV_EUNSUPPORTED;
   return e == cudaSuccess ? CONV_OK : CONV_ELAUNCH;
 }
 
 int conv_causal_grad_workspace_size(int N, long long L, int C, int K, int packed, unsigned long long* bytes) {
   if (!shape_ok(N, L, C, K, packed != 0) || !bytes) return CONV_EINVAL;
-  const long long runs = (L + kGradRun - 1) / kGradRun * (packed ? 1 : N);
-  // the narrowest vectors have the most blocks along the channels and so the fewest along the runs: the widest decide
-  *bytes = 4ull * grad_blocks_y(C, 4, runs) * (K + 1) * C;
+  *bytes = 4ull * run_blocks(N, L, grad_run(N, L, C, packed != 0), packed != 0) * (K + 1) * C;
   return CONV_OK;
 }
 
@@ -167,33 +165,29 @@ int conv_causal_grad(const void* x, const unsigned char* x_scale, const void* w,
   outs[4] = span_of(workspace, static_cast<long long>(need));
   if (any_alias(outs, 5, ins, 9)) return CONV_EALIAS;
   CausalArgs a = {};
-  a.x = x, a.w = w, a.bias = bias, a.state = state, a.cu = cu, a.dy = dy, a.x_scale = x_scale;
+  a.x = SeqIn{x, x_scale, x_batch, x_token}, a.dy = SeqIn{dy, nullptr, dy_batch, dy_token};
+  a.w = w, a.bias = bias, a.state = state, a.cu = cu;
   a.dstate_out = window > 0 ? dstate_out : nullptr;
   a.dx = dx, a.dw = dw, a.dbias = dbias, a.dstate = dstate, a.part = static_cast<float*>(workspace);
   a.N = N, a.C = C, a.K = K, a.silu = activation == CONV_ACT_SILU, a.fill = fill != 0;
-  a.L = L, a.x_batch = x_batch, a.x_token = x_token, a.dy_batch = dy_batch, a.dy_token = dy_token;
-  a.run = kGradRun;
-  a.runs = (L + a.run - 1) / a.run;
+  a.L = static_cast<int>(L);
+  a.run = grad_run(N, L, C, packed);
+  a.runs = static_cast<int>((L + a.run - 1) / a.run);
+  const long long by = run_blocks(N, L, a.run, packed);
+  if (by > 65535) return CONV_EUNSUPPORTED;
+  const dim3 grid((C + 63) / 64, static_cast<unsigned>(by));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = by_type_and_taps(dtype, K, [&](auto t, auto kt) {
     using T = typename decltype(t)::type;
-    constexpr int KT = decltype(kt)::value, V = KT == 8 ? 2 : 4;
-    const size_t bytes = V * sizeof(T);
-    const bool vec =
-        C % V == 0 &&
-        (x_scale ? rows_aligned(x, packed ? 0 : x_batch, x_token, 1, V)
-                 : rows_aligned(x, packed ? 0 : x_batch, x_token, es, bytes)) &&
-        rows_aligned(dy, packed ? 0 : dy_batch, dy_token, es, bytes) && aligned_to(dx, bytes) &&
-        aligned_to(state, bytes) && aligned_to(dstate_out, bytes);
-    const int v = vec ? V : 1;
-    const int by = grad_blocks_y(C, v, a.runs * (packed ? 1 : N));
-    const dim3 grid(((C + v - 1) / v + kGradLanes - 1) / kGradLanes, by), block(kGradLanes, kGradRows);
-    auto* k = x_scale ? (vec ? conv_causal_grad_kernel<T, KT, V, true> : conv_causal_grad_kernel<T, KT, 1, true>)
-                      : (vec ? conv_causal_grad_kernel<T, KT, V, false> : conv_causal_grad_kernel<T, KT, 1, false>);
-    cudaError_t err = launch_pdl(k, grid, block, 0, st, 1, a);
+    constexpr int KT = decltype(kt)::value;
+    const bool aligned = aligned_rows(a.x, packed, C, es) && aligned_rows(a.dy, packed, C, es) && aligned_to(dx, 2 * es);
+    auto* k = x_scale ? (aligned ? conv_causal_grad_kernel<T, KT, true, true> : conv_causal_grad_kernel<T, KT, false, true>)
+                      : (aligned ? conv_causal_grad_kernel<T, KT, true, false> : conv_causal_grad_kernel<T, KT, false, false>);
+    cudaError_t err = launch_rows(k, grid, sizeof(CausalGradShared<T>), a, st);
     if (err != cudaSuccess) return err;
-    err = launch_pdl(conv_causal_sum_kernel<T>, dim3((C + 255) / 256, K + 1), dim3(256), 0, st, 1,
-                     static_cast<const float*>(a.part), static_cast<T*>(dw), static_cast<T*>(dbias), by, C, K);
+    err = launch_pdl(conv_causal_sum_kernel<T>, dim3((C + 31) / 32, K + 1), dim3(32, 8), 0, st, 1,
+                     static_cast<const float*>(a.part), static_cast<T*>(dw), static_cast<T*>(dbias), static_cast<int>(by), C,
+                     K);
     if (err != cudaSuccess || !dstate || window == 0) return err;
     return launch_pdl(x_scale ? conv_causal_dstate_kernel<T, true> : conv_causal_dstate_kernel<T, false>,
                       dim3((C + 127) / 128, std::min(N, 65535)), dim3(128), 0, st, 1, a);

@@ -3,344 +3,458 @@
 //
 //   z[t] = bias + sum_{o < K} w[K-1-o] x[t-o],   y = z or z * sigmoid(z)
 //
-// A thread owns V neighbouring channels and a run of tokens, and keeps the
-// K - 1 rows in front of the current one in registers, so x is read once from
-// memory (and K - 1 rows a run once more, out of L2).  Where a sequence begins
-// the rows in the registers become that sequence's window, so no later token
-// needs to know where it began.
+// A warp owns 64 channels and a run of tokens, two channels a lane, whose
+// arithmetic is packed.  Its rows come through shared memory (seq_tile.cuh), and
+// the K - 1 rows in front of the current ones stay in registers, so x is read
+// once from memory (and K - 1 rows a run once more, out of L2).  Where a sequence
+// begins the rows in the registers become that sequence's window, so no later
+// token needs to know where it began.
 //
-// KT is the least of 2, 3, 4 and 8 that holds K; taps behind K are skipped, not multiplied
-// by zero, as x may be infinite there.
+// KT is the least of 2, 3, 4 and 8 that holds K; taps behind K are skipped, not
+// multiplied by zero, as x may be infinite there.
 #pragma once
 
-#include "seq_common.cuh"
+#include "seq_tile.cuh"
 
 namespace convfwd {
 
 struct CausalArgs {
-  const void *x, *w, *bias, *state, *dy, *dstate_out;
-  const unsigned char* x_scale;
+  SeqIn x, dy;
+  const void *w, *bias, *state, *dstate_out;
   const int* cu;
   void *y, *state_out, *dx, *dw, *dbias, *dstate;
   float* part;
   int N, C, K, silu, fill;
-  long long L, x_batch, x_token, dy_batch, dy_token;
-  int run;         // tokens of a thread's run
-  long long runs;  // runs of a sequence (packed: of all rows)
+  int L;      // tokens of a sequence (packed: all rows)
+  int run;    // tokens of a warp's run
+  int runs;   // runs of a sequence (packed: of all rows)
 };
 
-__device__ __forceinline__ float causal_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
-
-// The sequence of a token, as the threads walk along it.
+// The sequence of a token, as the warps walk along it.
 struct SeqAt {
-  int s;                 // its number, N where the row is in none
-  long long begin, end;  // its first token and the one behind its last
+  int s;           // its number, N where the row is in none
+  int begin, end;  // its first token and the one behind its last
 };
 
-__device__ __forceinline__ void seq_find(SeqAt& q, const CausalArgs& a, long long t) {
+__device__ __forceinline__ void seq_find(SeqAt& q, const CausalArgs& a, int t) {
   q.s = seq_of_row(a.cu, a.N, t);
   if (q.s < a.N) {
     q.begin = max(0, __ldg(a.cu + q.s));
-    q.end = min(a.L, static_cast<long long>(__ldg(a.cu + q.s + 1)));
+    q.end = min(a.L, __ldg(a.cu + q.s + 1));
   } else {  // unused rows: up to the next sequence's first token, or the end
-    const long long first = a.N > 0 ? __ldg(a.cu) : 0;
+    const int first = a.N > 0 ? __ldg(a.cu) : 0;
     q.begin = t;
     q.end = t < first ? min(a.L, first) : a.L;
   }
 }
 
-// V channels of row t of x.
+// `width` (V at most) channels from c on of row t of sequence q of x, or of its
+// window where t is in front of it; zeros behind them.
 template <typename T, int V, bool Q8>
-struct XRow {
-  using R = typename RawVec<Q8 ? V : static_cast<int>(sizeof(T)) * V>::type;
-  R raw;
-  unsigned char byte;
-  __device__ __forceinline__ void load(const CausalArgs& a, int n, long long t, int c) {
-    const long long at = n * a.x_batch + t * a.x_token + c;
-    if constexpr (Q8) {
-      raw = __ldg(reinterpret_cast<const R*>(static_cast<const signed char*>(a.x) + at));
-      const long long row = n * a.L + t;
-      byte = __ldg(a.x_scale + row * ((a.C + ACT8_BLOCK - 1) / ACT8_BLOCK) + c / ACT8_BLOCK);
-    } else {
-      raw = __ldg(reinterpret_cast<const R*>(static_cast<const T*>(a.x) + at));
-    }
-  }
-  __device__ __forceinline__ void get(float (&v)[V]) const {
-    if constexpr (Q8) {
-      union {
-        R r;
-        signed char e[V];
-      } u;
-      u.r = raw;
-      const float step = act8_step(byte);
-#pragma unroll
-      for (int k = 0; k < V; ++k) v[k] = static_cast<float>(u.e[k]) * step;
-    } else {
-      unpack<T, V>(raw, v);
-    }
-  }
-};
-
-// Row `t` of sequence q of x, or of its window where t is in front of it.
-template <typename T, int V, bool Q8>
-__device__ __forceinline__ void row_or_window(float (&v)[V], const CausalArgs& a, int n, const SeqAt& q, long long t,
-                                              int c) {
-  if (t >= q.begin) {
-    XRow<T, V, Q8> x;
-    x.load(a, n, t, c);
-    x.get(v);
-  } else if (a.state && q.s < a.N && t >= q.begin - (a.K - 1)) {
-    const long long row = static_cast<long long>(q.s) * (a.K - 1) + (a.K - 1 + t - q.begin);
-    unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.state) + row * a.C + c), v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < V; ++k) v[k] = 0.f;
-  }
-}
-
-// w[c + k][K-1-o] in w[o][k], and the bias.
-template <typename T, int KT, int V>
-__device__ __forceinline__ void load_filter(float (&w)[KT][V], float (&bias)[V], const CausalArgs& a, int c) {
+__device__ __forceinline__ Vf<V> row_or_window(const CausalArgs& a, int n, const SeqAt& q, int t, int c, int width) {
+  Vf<V> v = splat<V>(0.f);
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    bias[k] = a.bias ? to_f32<T>(static_cast<const T*>(a.bias)[c + k]) : 0.f;
+    if (k >= width) continue;
+    if (t >= q.begin) {
+      const long long at = n * a.x.batch + t * a.x.token + c + k;
+      if constexpr (Q8) {
+        const long long row = static_cast<long long>(n) * a.L + t;
+        v[k] = static_cast<float>(static_cast<const signed char*>(a.x.p)[at]) *
+               act8_step(__ldg(a.x.scale + row * ((a.C + ACT8_BLOCK - 1) / ACT8_BLOCK) + (c + k) / ACT8_BLOCK));
+      } else {
+        v[k] = to_f32<T>(__ldg(static_cast<const T*>(a.x.p) + at));
+      }
+    } else if (a.state && q.s < a.N && t >= q.begin - (a.K - 1)) {
+      const long long row = static_cast<long long>(q.s) * (a.K - 1) + (a.K - 1 + t - q.begin);
+      v[k] = to_f32<T>(__ldg(static_cast<const T*>(a.state) + row * a.C + c + k));
+    }
+  }
+  return v;
+}
+
+// w[c + k][K-1-o] in w[o][k], and the bias; zeros behind `width` channels.
+template <typename T, int KT, int V>
+__device__ __forceinline__ void load_filter(Vf<V> (&w)[KT], Vf<V>& bias, const void* wp, const void* bp, int K, int c, int width) {
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const bool in = k < width;
+    bias[k] = bp && in ? to_f32<T>(static_cast<const T*>(bp)[c + k]) : 0.f;
 #pragma unroll
     for (int o = 0; o < KT; ++o)
-      w[o][k] = o < a.K ? to_f32<T>(static_cast<const T*>(a.w)[static_cast<long long>(c + k) * a.K + a.K - 1 - o]) : 0.f;
+      w[o][k] = o < K && in ? to_f32<T>(static_cast<const T*>(wp)[static_cast<long long>(c + k) * K + K - 1 - o]) : 0.f;
   }
 }
 
-constexpr int kCausalThreads = 256;
-constexpr int kCausalAhead = 4;  // rows loaded ahead of their use
+// Whether tap o exists: where KT is not K itself, known only now.
+template <int KT>
+__device__ __forceinline__ bool has_tap(int o, int K) {
+  return KT == 3 || KT == 4 || o < K;
+}
 
-template <typename T, int KT, int V>
-__global__ void __launch_bounds__(kCausalThreads) conv_causal_kernel(const CausalArgs a) {
+// sigmoid(z), and silu's slope s (1 + z (1 - s))
+template <int V>
+__device__ __forceinline__ Vf<V> sigmoid_v(const Vf<V>& z) {
+  Vf<V> s;
+#pragma unroll
+  for (int k = 0; k < V; ++k) s[k] = rcp_approx(1.f + ex2_approx(z[k] * -kLog2e));
+  return s;
+}
+template <int V>
+__device__ __forceinline__ Vf<V> silu_slope(const Vf<V>& z) {
+  const Vf<V> s = sigmoid_v(z);
+  Vf<V> r;
+#pragma unroll
+  for (int k = 0; k < V; ++k) r[k] = 1.f - s[k];
+  r = mul_v(z, r);
+  return fma_v(s, r, s);
+}
+
+constexpr int kCausalWarps = 8;
+constexpr int kCausalThreads = 32 * kCausalWarps;
+// Rows of a tile (2 KB), and tokens that are computed together: their rows move
+// through registers, which unrolled steps rename rather than copy.
+template <typename T>
+constexpr int kCausalRows = 32 / static_cast<int>(sizeof(T));
+constexpr int kCausalTogether = 8;
+
+template <typename T>
+struct CausalShared {
+  RowTile<T, kCausalRows<T>> x[kCausalWarps][2];  // the rows at hand and the next
+};
+
+template <int LEFT>
+__device__ __forceinline__ void groups_done() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ void group_ends() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <typename T, int KT, bool ALIGNED>
+__global__ void __launch_bounds__(kCausalThreads) conv_causal_kernel(const __grid_constant__ CausalArgs a) {
+  constexpr int V = 2, ROWS = kCausalRows<T>, U = kCausalTogether, W = KT - 1;
+  extern __shared__ __align__(128) unsigned char smem[];
+  CausalShared<T>& sh = *reinterpret_cast<CausalShared<T>*>(smem);
   ptx::pdl_wait_prev();
-  const int nvec = a.C / V;
-  const long long id = static_cast<long long>(blockIdx.x) * kCausalThreads + threadIdx.x;
-  T* y = static_cast<T*>(a.y);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c0 = blockIdx.x * 64, c = c0 + lane * V, there = a.C - c0;
+  const int width = min(V, a.C - c);
+  const bool in = width > 0;
+  const long long job = static_cast<long long>(blockIdx.y) * kCausalWarps + warp;
   T* state_out = static_cast<T*>(a.state_out);
-  if (state_out) {
+  if (state_out && in) {
     // sequences without a token leave their window as it was
-    const long long all = static_cast<long long>(gridDim.x) * kCausalThreads;
-    for (long long k = id; k < static_cast<long long>(a.N) * nvec; k += all) {
-      const int s = static_cast<int>(k / nvec), c = static_cast<int>(k - static_cast<long long>(s) * nvec) * V;
+    for (long long s = job; s < a.N; s += static_cast<long long>(gridDim.y) * kCausalWarps) {
       if (a.cu ? __ldg(a.cu + s) < __ldg(a.cu + s + 1) : a.L > 0) continue;
-      for (int j = 0; j < a.K - 1; ++j) {
-        const long long at = (static_cast<long long>(s) * (a.K - 1) + j) * a.C + c;
-        float v[V] = {};
-        if (a.state) unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.state) + at), v);
-        store_vec<T, V>(state_out + at, v);
-      }
+      const SeqAt q{static_cast<int>(s), 0, 0};
+      for (int j = 0; j < a.K - 1; ++j)
+        put_row<T, V, ALIGNED>(state_out + (s * (a.K - 1) + j) * a.C + c, width,
+                               row_or_window<T, V, false>(a, 0, q, j - (a.K - 1), c, width));
     }
   }
-  const long long run = id / nvec;
-  if (run >= a.runs * (a.cu ? 1 : a.N)) return;
-  const int c = static_cast<int>(id - run * nvec) * V;
-  const int n = a.cu ? 0 : static_cast<int>(run / a.runs);
-  const long long t0 = (run - n * a.runs) * a.run, t1 = min(a.L, t0 + a.run);
+  if (job >= static_cast<long long>(a.runs) * (a.cu ? 1 : a.N)) return;
+  const int n = a.cu ? 0 : static_cast<int>(job / a.runs);
+  const int t0 = static_cast<int>(job - static_cast<long long>(n) * a.runs) * a.run, t1 = min(a.L, t0 + a.run);
 
-  float w[KT][V], bias[V], old[KT - 1][V];  // old[o]: row t - 1 - o
-  load_filter<T, KT, V>(w, bias, a, c);
+  TileWalk<T, ROWS, ALIGNED> walk;
+  walk.start(a.x, n, t0, c0);
+  auto& tile = sh.x[warp];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    walk.load(tile[k], t1 - t0 - k * ROWS, there);
+    walk.next(ROWS);
+    group_ends();
+  }
+  Vf<V> w[KT], bias, X[W + U];  // X[W + u]: row t + u
+  load_filter<T, KT, V>(w, bias, a.w, a.bias, a.K, c, width);
   SeqAt q{n, 0, a.L};
   if (a.cu) seq_find(q, a, t0);
 #pragma unroll
-  for (int o = 0; o < KT - 1; ++o) row_or_window<T, V, false>(old[o], a, n, q, t0 - 1 - o, c);
+  for (int o = 1; o <= W; ++o) X[W - o] = row_or_window<T, V, false>(a, n, q, t0 - o, c, width);
 
-  for (long long t = t0; t < t1; t += kCausalAhead) {
-    XRow<T, V, false> ahead[kCausalAhead];
+  T* out = static_cast<T*>(a.y) + (static_cast<long long>(n) * a.L + t0) * a.C + c;
+  const auto put = [&](T* p, const Vf<V>& z) {
+    if (in) put_row<T, V, ALIGNED>(p, width, z);
+  };
+  const auto compute = [&](int u) {
+    Vf<V> z = fma_v(w[0], X[W + u], bias);
 #pragma unroll
-    for (int u = 0; u < kCausalAhead; ++u)
-      if (t + u < t1) ahead[u].load(a, n, t + u, c);
+    for (int o = 1; o < KT; ++o)
+      if (has_tap<KT>(o, a.K)) z = fma_v(w[o], X[W + u - o], z);
+    return z;
+  };
+  int b = 0;
+  for (int t = t0; t < t1; t += ROWS, b ^= 1) {
+    groups_done<1>();
+#pragma unroll 1
+    for (int r = 0; r < ROWS; r += U, out += static_cast<long long>(U) * a.C) {
 #pragma unroll
-    for (int u = 0; u < kCausalAhead; ++u) {
-      if (t + u >= t1) break;
-      if (t + u >= q.end) {
-        seq_find(q, a, t + u);
+      for (int u = 0; u < U; ++u) unpack<T, V>(row_pair(tile[b], r + u, lane), X[W + u].v);
+      const int at = t + r;
+      if (q.s < a.N && at + U <= t1 && at + U < q.end + (state_out ? 0 : 1)) {
+        T* p = out;
+        if (a.silu) {
 #pragma unroll
-        for (int o = 0; o < KT - 1; ++o) row_or_window<T, V, false>(old[o], a, n, q, t + u - 1 - o, c);
+          for (int u = 0; u < U; ++u, p += a.C) {
+            const Vf<V> z = compute(u);
+            put(p, mul_v(z, sigmoid_v(z)));
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u, p += a.C) put(p, compute(u));
+        }
+      } else {
+        // a sequence or the run ends here
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (at + u >= t1) break;
+          if (at + u >= q.end) {
+            seq_find(q, a, at + u);
+#pragma unroll
+            for (int o = 1; o <= W; ++o) X[W + u - o] = row_or_window<T, V, false>(a, n, q, at + u - o, c, width);
+          }
+          T* p = out + static_cast<long long>(u) * a.C;
+          if (q.s < a.N) {
+            const Vf<V> z = compute(u);
+            put(p, a.silu ? mul_v(z, sigmoid_v(z)) : z);
+          } else if (a.fill) {
+            put(p, splat<V>(0.f));
+          }
+          if (state_out && q.s < a.N && at + u == q.end - 1) {
+#pragma unroll
+            for (int o = 0; o < W; ++o)
+              if (o < a.K - 1) put(state_out + (static_cast<long long>(q.s) * (a.K - 1) + a.K - 2 - o) * a.C + c, X[W + u - o]);
+          }
+        }
       }
-      float x[V], z[V];
-      ahead[u].get(x);
 #pragma unroll
-      for (int k = 0; k < V; ++k) z[k] = fmaf(w[0][k], x[k], bias[k]);
-#pragma unroll
-      for (int o = 1; o < KT; ++o)
-        if (o < a.K)
-#pragma unroll
-          for (int k = 0; k < V; ++k) z[k] = fmaf(w[o][k], old[o - 1][k], z[k]);
-#pragma unroll
-      for (int o = KT - 2; o > 0; --o)
-#pragma unroll
-        for (int k = 0; k < V; ++k) old[o][k] = old[o - 1][k];
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        old[0][k] = x[k];
-        if (a.silu) z[k] = z[k] * causal_sigmoid(z[k]);
-      }
-      T* out = y + (n * a.L + t + u) * a.C + c;
-      if (q.s < a.N) store_vec<T, V>(out, z);
-      else if (a.fill) store_zero<T, V>(out);
-      if (state_out && q.s < a.N && t + u == q.end - 1) {
-#pragma unroll
-        for (int o = 0; o < KT - 1; ++o)
-          if (o < a.K - 1)
-            store_vec<T, V>(state_out + (static_cast<long long>(q.s) * (a.K - 1) + a.K - 2 - o) * a.C + c, old[o]);
-      }
+      for (int i = 0; i < W; ++i) X[i] = X[i + U];
     }
+    __syncwarp();
+    walk.load(tile[b], t1 - t - 2 * ROWS, there);
+    walk.next(ROWS);
+    group_ends();
   }
-}
-
-// d silu(z) / dz
-__device__ __forceinline__ float silu_slope(float z) {
-  const float s = causal_sigmoid(z);
-  return s * fmaf(z, 1.f - s, 1.f);
+  groups_done<0>();
 }
 
 // ---- gradients ----------------------------------------------------------
 //
-// A thread walks its run and the K - 1 tokens behind it: z is computed again
-// from x, dz[t] = dy[t] * (slope of the activation), and each dz[t] goes to the
-// K rows of dx that token t read.  Those are complete once dz[t+K-1] is in, so
-// the pending ones (`next`) live in registers like the rows of x.  dw and dbias
-// of the run's own tokens are summed per run, runs into the thread's total,
-// threads of a block in shared memory in order, and blocks by
-// conv_causal_sum_kernel in order.
-constexpr int kGradLanes = 32, kGradRows = 8;  // a block: 32 vectors of channels x 8 runs
+// A warp walks its run and the K - 1 tokens behind it: z is computed again from
+// x, dz[t] = dy[t] * (slope of the activation), and each dz[t] goes to the K rows
+// of dx that token t read.  A row is complete once the token K - 1 behind it is
+// in, so the pending rows of dx move through registers like the rows of x.
+//
+// dw and dbias of the run's own tokens are summed per warp, the block's warps in
+// shared memory in order, and blocks by conv_causal_sum_kernel in order.
+constexpr int kGradTogether = 4;
 
-template <typename T, int KT, int V, bool Q8>
-__global__ void __launch_bounds__(kGradLanes * kGradRows) conv_causal_grad_kernel(const CausalArgs a) {
-  ptx::pdl_wait_prev();
-  const int c = (blockIdx.x * kGradLanes + threadIdx.x) * V;
-  const long long all_runs = a.runs * (a.cu ? 1 : a.N);
-  T* dx = static_cast<T*>(a.dx);
-  float dw_sum[KT][V] = {}, db_sum[V] = {};
-  if (c < a.C) {
-    float w[KT][V], bias[V];
-    load_filter<T, KT, V>(w, bias, a, c);
-    for (long long run = static_cast<long long>(blockIdx.y) * kGradRows + threadIdx.y; run < all_runs;
-         run += static_cast<long long>(gridDim.y) * kGradRows) {
-      const int n = a.cu ? 0 : static_cast<int>(run / a.runs);
-      const long long t0 = (run - n * a.runs) * a.run, t1 = min(a.L, t0 + a.run), t2 = min(a.L, t1 + a.K - 1);
-      float old[KT - 1][V], next[KT][V] = {}, dw[KT][V] = {}, db[V] = {};  // next[o]: dx of row t - o
-      SeqAt q{n, 0, a.L};
-      if (a.cu) seq_find(q, a, t0);
+template <typename T>
+struct CausalGradShared {
+  struct {
+    RowTile<T, kCausalRows<T>> x, dy;
+  } tile[kCausalWarps][2];
+};
+
+// A lane's registers.
+template <typename T, int KT, bool Q8>
+struct GradRegs {
+  static constexpr int V = 2, U = kGradTogether, W = KT - 1;
+  Vf<V> w[KT], bias, X[W + U], D[W + U], dw[KT], db;  // X[W + u], D[W + u]: rows t + u of x and dx
+  unsigned used;                                       // bit i: row t - W + i is in a sequence, and the run's
+  SeqAt q;
+
+  // Token t + u of those together, its row of x and of dy.  EDGE: a sequence's or
+  // the run's end, or the window's gradient, may touch it.  t1: behind the run;
+  // t2: behind the last token that reads a row of it.
+  template <bool EDGE>
+  __device__ __forceinline__ void token(const CausalArgs& a, int n, int u, int t, int t1, int t2, int c, int width,
+                                        const Raw<T, V>& x, const Raw<T, V>& dy) {
+    X[W + u] = D[W + u] = splat<V>(0.f);
+    int pos = KT;
+    if (EDGE) {
+      if (t + u >= t2) return;
+      if (t + u >= q.end) {
+        seq_find(q, a, t + u);
 #pragma unroll
-      for (int o = 0; o < KT - 1; ++o) row_or_window<T, V, Q8>(old[o], a, n, q, t0 - 1 - o, c);
-      bool used[KT] = {};  // of row t - o
-      for (long long t = t0; t < t1 + a.K - 1; ++t) {
-        // next[] moves on by a row: the one of t begins
-#pragma unroll
-        for (int o = KT - 1; o > 0; --o) {
-          used[o] = used[o - 1];
-#pragma unroll
-          for (int k = 0; k < V; ++k) next[o][k] = next[o - 1][k];
-        }
-        used[0] = false;
-#pragma unroll
-        for (int k = 0; k < V; ++k) next[0][k] = 0.f;
-        if (t < t2) {
-          if (t >= q.end) {
-            seq_find(q, a, t);
-#pragma unroll
-            for (int o = 0; o < KT - 1; ++o) row_or_window<T, V, Q8>(old[o], a, n, q, t - 1 - o, c);
-          }
-          used[0] = q.s < a.N;
-          if (used[0]) {
-            XRow<T, V, Q8> xr;
-            xr.load(a, n, t, c);
-            float x[V], dz[V];
-            xr.get(x);
-            unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.dy) + n * a.dy_batch + t * a.dy_token + c), dz);
-            if (a.silu) {
-              float z[V];
-#pragma unroll
-              for (int k = 0; k < V; ++k) z[k] = fmaf(w[0][k], x[k], bias[k]);
-#pragma unroll
-              for (int o = 1; o < KT; ++o)
-                if (o < a.K)
-#pragma unroll
-                  for (int k = 0; k < V; ++k) z[k] = fmaf(w[o][k], old[o - 1][k], z[k]);
-#pragma unroll
-              for (int k = 0; k < V; ++k) dz[k] *= silu_slope(z[k]);
-            }
-            if (t < t1) {
-#pragma unroll
-              for (int k = 0; k < V; ++k) db[k] += dz[k], dw[0][k] = fmaf(dz[k], x[k], dw[0][k]);
-#pragma unroll
-              for (int o = 1; o < KT; ++o)
-                if (o < a.K)
-#pragma unroll
-                  for (int k = 0; k < V; ++k) dw[o][k] = fmaf(dz[k], old[o - 1][k], dw[o][k]);
-            }
-            const long long slot = t - q.end + a.K - 1;  // of the window that the sequence leaves
-            if (a.dstate_out && slot >= 0) {
-              const long long row = static_cast<long long>(q.s) * (a.K - 1) + slot;
-              unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.dstate_out) + row * a.C + c), next[0]);
-            }
-            const long long pos = t - q.begin;
-#pragma unroll
-            for (int o = 0; o < KT; ++o)
-              if (o < a.K && o <= pos)
-#pragma unroll
-                for (int k = 0; k < V; ++k) next[o][k] = fmaf(w[o][k], dz[k], next[o][k]);
-#pragma unroll
-            for (int o = KT - 2; o > 0; --o)
-#pragma unroll
-              for (int k = 0; k < V; ++k) old[o][k] = old[o - 1][k];
-#pragma unroll
-            for (int k = 0; k < V; ++k) old[0][k] = x[k];
-          }
-        }
-        const long long done = t - (a.K - 1);
-        if (done >= t0 && done < t1) {
-          T* out = dx + (n * a.L + done) * a.C + c;
-#pragma unroll
-          for (int o = 0; o < KT; ++o)
-            if (o == a.K - 1) {
-              if (used[o]) store_vec<T, V>(out, next[o]);
-              else if (a.fill) store_zero<T, V>(out);
-            }
-        }
+        for (int o = 1; o <= W; ++o) X[W + u - o] = row_or_window<T, V, Q8>(a, n, q, t + u - o, c, width);
       }
+      if (q.s >= a.N) return;
+      pos = min(t + u - q.begin, KT);
+      const int slot = t + u - q.end + a.K - 1;  // of the window that the sequence leaves
+      if (a.dstate_out && slot >= 0) {
+        const T* g = static_cast<const T*>(a.dstate_out) + (static_cast<long long>(q.s) * (a.K - 1) + slot) * a.C + c;
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        db_sum[k] += db[k];
-#pragma unroll
-        for (int o = 0; o < KT; ++o) dw_sum[o][k] += dw[o][k];
+        for (int k = 0; k < V; ++k)
+          if (k < width) D[W + u][k] = to_f32<T>(__ldg(g + k));
       }
     }
+    const bool own = !EDGE || t + u < t1;
+    if (own) used |= 1u << (W + u);
+    Vf<V> dz;
+    unpack<T, V>(x, X[W + u].v);
+    unpack<T, V>(dy, dz.v);
+    if (a.silu) {
+      Vf<V> z = fma_v(w[0], X[W + u], bias);
+#pragma unroll
+      for (int o = 1; o < KT; ++o)
+        if (has_tap<KT>(o, a.K)) z = fma_v(w[o], X[W + u - o], z);
+      dz = mul_v(dz, silu_slope(z));
+    }
+    if (own) {
+      db = add_v(db, dz);
+#pragma unroll
+      for (int o = 0; o < KT; ++o)
+        if (has_tap<KT>(o, a.K)) dw[o] = fma_v(dz, X[W + u - o], dw[o]);
+    }
+#pragma unroll
+    for (int o = 0; o < KT; ++o)
+      if (has_tap<KT>(o, a.K) && (!EDGE || o <= pos)) D[W + u - o] = fma_v(w[o], dz, D[W + u - o]);
   }
-  // the block's eight threads of each channel, in order
-  __shared__ float sums[kGradRows][kGradLanes * V];
+};
+
+template <typename T, int KT, bool ALIGNED, bool Q8>
+__global__ void __launch_bounds__(kCausalThreads, 2) conv_causal_grad_kernel(const __grid_constant__ CausalArgs a) {
+  constexpr int V = 2, ROWS = kCausalRows<T>, U = kGradTogether, W = KT - 1;
+  extern __shared__ __align__(128) unsigned char smem[];
+  CausalGradShared<T>& sh = *reinterpret_cast<CausalGradShared<T>*>(smem);
+  ptx::pdl_wait_prev();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c0 = blockIdx.x * 64, c = c0 + lane * V, there = a.C - c0;
+  const int width = min(V, a.C - c);
+  const bool in = width > 0;
+  const long long job = static_cast<long long>(blockIdx.y) * kCausalWarps + warp;
+  GradRegs<T, KT, Q8> k;
+  k.db = splat<V>(0.f);
+#pragma unroll
+  for (int o = 0; o < KT; ++o) k.dw[o] = splat<V>(0.f);
+  if (job < static_cast<long long>(a.runs) * (a.cu ? 1 : a.N)) {
+    const int n = a.cu ? 0 : static_cast<int>(job / a.runs);
+    const int t0 = static_cast<int>(job - static_cast<long long>(n) * a.runs) * a.run, t1 = min(a.L, t0 + a.run);
+    const int t2 = min(a.L, t1 + a.K - 1);  // behind the last token that reads a row of the run
+    TileWalk<T, ROWS, ALIGNED> walk, walk_dy;
+    TileWalk<signed char, ROWS, ALIGNED> walk8;
+    const unsigned char* steps = nullptr;  // of the lane's row and block (see expand8)
+    const int nblk = (a.C + ACT8_BLOCK - 1) / ACT8_BLOCK;
+    if constexpr (Q8) {
+      walk8.start(a.x, n, t0, c0);
+      steps = a.x.scale + (static_cast<long long>(n) * a.L + t0 + lane / 4) * nblk + c0 / ACT8_BLOCK + lane % 4 / 2;
+    } else {
+      walk.start(a.x, n, t0, c0);
+    }
+    walk_dy.start(a.dy, n, t0, c0);
+    int byte[2][ROWS / 8] = {};
+    const auto load = [&](int b, int rows) {
+      auto& tile = sh.tile[warp][b];
+      if constexpr (Q8) {
+        // bytes of eight rows at the beginning of each eight rows of the tile
+        walk8.load(reinterpret_cast<RowTile<signed char, ROWS>&>(tile.x), rows, there);
+        walk8.next(ROWS);
+#pragma unroll
+        for (int e = 0; e < ROWS / 8; ++e) {
+          byte[b][e] = 0;
+          if (lane / 4 + 8 * e < rows && lane % 4 / 2 * ACT8_BLOCK < there) byte[b][e] = __ldg(steps + 8 * e * nblk);
+        }
+        steps += ROWS * nblk;
+      } else {
+        walk.load(tile.x, rows, there);
+        walk.next(ROWS);
+      }
+      walk_dy.load(tile.dy, rows, there);
+      walk_dy.next(ROWS);
+      group_ends();
+    };
+    load(0, t2 - t0);
+    load(1, t2 - t0 - ROWS);
+    load_filter<T, KT, V>(k.w, k.bias, a.w, a.bias, a.K, c, width);
+    k.used = 0;
+    k.q = SeqAt{n, 0, a.L};
+    if (a.cu) seq_find(k.q, a, t0);
+#pragma unroll
+    for (int o = 1; o <= W; ++o) {
+      k.X[W - o] = row_or_window<T, V, Q8>(a, n, k.q, t0 - o, c, width);
+      k.D[W - o] = splat<V>(0.f);
+    }
+    T* out = static_cast<T*>(a.dx) + (static_cast<long long>(n) * a.L + t0 - W) * a.C + c;  // row t - W
+
+    int b = 0;
+    for (int t = t0; t < t1 + W; t += ROWS, b ^= 1) {
+      groups_done<1>();
+      auto& tile = sh.tile[warp][b];
+      if constexpr (Q8) {
+#pragma unroll
+        for (int e = ROWS / 8 - 1; e >= 0; --e) {  // the bytes of later rows lie in front of their place
+          move8(tile.x, e);
+          expand8(tile.x, 8 * e, b ? byte[1][e] : byte[0][e]);
+        }
+      }
+#pragma unroll 1
+      for (int r = 0; r < ROWS; r += U, out += static_cast<long long>(U) * a.C) {
+        const int at = t + r;
+        const bool inside = k.q.s < a.N && at + U <= t1 && at - k.q.begin >= W &&
+                            at + U <= k.q.end - (a.dstate_out ? a.K - 1 : 0);
+        T* p = out;
+        if (inside) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            k.template token<false>(a, n, u, at, t1, t2, c, width, row_pair(tile.x, r + u, lane), row_pair(tile.dy, r + u, lane));
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            k.template token<true>(a, n, u, at, t1, t2, c, width, row_pair(tile.x, r + u, lane), row_pair(tile.dy, r + u, lane));
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i, p += a.C) {
+          if (in && (k.used >> i & 1)) put_row<T, V, ALIGNED>(p, width, k.D[i]);
+          else if (in && a.fill && at - W + i >= t0 && at - W + i < t1) put_row<T, V, ALIGNED>(p, width, splat<V>(0.f));
+        }
+        k.used >>= U;
+#pragma unroll
+        for (int i = 0; i < W; ++i) k.X[i] = k.X[i + U], k.D[i] = k.D[i + U];
+      }
+      __syncwarp();
+      load(b, t2 - t - 2 * ROWS);
+    }
+    groups_done<0>();
+  }
+  // the block's warps in order
+  __syncthreads();
+  Vf<V>(&sums)[kCausalWarps][32] = *reinterpret_cast<Vf<V>(*)[kCausalWarps][32]>(smem);
 #pragma unroll
   for (int o = 0; o <= KT; ++o) {
     if (o < KT && o >= a.K) continue;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < V; ++k) sums[threadIdx.y][threadIdx.x * V + k] = o < KT ? dw_sum[o < KT ? o : 0][k] : db_sum[k];
+    sums[warp][lane] = o < KT ? k.dw[o < KT ? o : 0] : k.db;
     __syncthreads();
     const int row = o < KT ? a.K - 1 - o : a.K;
-    for (int k = threadIdx.y * kGradLanes + threadIdx.x; k < kGradLanes * V; k += kGradLanes * kGradRows) {
-      const int ch = blockIdx.x * kGradLanes * V + k;
-      if (ch >= a.C) continue;
-      float sum = 0.f;
+    if (warp == 0 && in) {
+      Vf<V> sum = sums[0][lane];
 #pragma unroll
-      for (int r = 0; r < kGradRows; ++r) sum += sums[r][k];
-      a.part[(static_cast<long long>(blockIdx.y) * (a.K + 1) + row) * a.C + ch] = sum;
+      for (int r = 1; r < kCausalWarps; ++r) sum = add_v(sum, sums[r][lane]);
+      float* part = a.part + (static_cast<long long>(blockIdx.y) * (a.K + 1) + row) * a.C + c;
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < width) part[e] = sum[e];
     }
+    __syncthreads();
   }
 }
 
-// dw and dbias: the blocks' partial sums [blocks][K + 1][C] added in order.
+// dw and dbias: the blocks' partial sums [blocks][K + 1][C], a thread every 8th
+// of them in order, then the eight in order.
 template <typename T>
 __global__ void __launch_bounds__(256) conv_causal_sum_kernel(const float* __restrict__ part, T* dw, T* dbias, int blocks,
                                                               int C, int K) {
+  __shared__ float sums[8][32];
   ptx::pdl_wait_prev();
-  const int c = blockIdx.x * 256 + threadIdx.x, j = blockIdx.y;
-  if (c >= C) return;
+  const int c = blockIdx.x * 32 + threadIdx.x, j = blockIdx.y;
   float sum = 0.f;
-  for (int b = 0; b < blocks; ++b) sum += part[(static_cast<long long>(b) * (K + 1) + j) * C + c];
+  if (c < C)
+    for (int b = threadIdx.y; b < blocks; b += 8) sum += part[(static_cast<long long>(b) * (K + 1) + j) * C + c];
+  sums[threadIdx.y][threadIdx.x] = sum;
+  __syncthreads();
+  if (threadIdx.y != 0 || c >= C) return;
+#pragma unroll
+  for (int r = 1; r < 8; ++r) sum += sums[r][threadIdx.x];
   if (j < K) dw[static_cast<long long>(c) * K + j] = from_f32<T>(sum);
   else if (dbias) dbias[c] = from_f32<T>(sum);
 }
@@ -348,7 +462,7 @@ __global__ void __launch_bounds__(256) conv_causal_sum_kernel(const float* __res
 // dstate: the window's rows are read by a sequence's first K - 1 tokens, and
 // passed on by a sequence of fewer.  A thread a (sequence, channel).
 template <typename T, bool Q8>
-__global__ void __launch_bounds__(128) conv_causal_dstate_kernel(const CausalArgs a) {
+__global__ void __launch_bounds__(128) conv_causal_dstate_kernel(const __grid_constant__ CausalArgs a) {
   ptx::pdl_wait_prev();
   const int c = blockIdx.x * 128 + threadIdx.x, K = a.K;
   if (c >= a.C) return;
@@ -356,26 +470,22 @@ __global__ void __launch_bounds__(128) conv_causal_dstate_kernel(const CausalArg
     const int n = a.cu ? 0 : s;
     SeqAt q{s, 0, a.L};
     if (a.cu) {
-      q.begin = max(0LL, min(a.L, static_cast<long long>(__ldg(a.cu + s))));
-      q.end = max(q.begin, min(a.L, static_cast<long long>(__ldg(a.cu + s + 1))));
+      q.begin = max(0, min(a.L, __ldg(a.cu + s)));
+      q.end = max(q.begin, min(a.L, __ldg(a.cu + s + 1)));
     }
-    const int len = static_cast<int>(min(q.end - q.begin, static_cast<long long>(K - 1)));
+    const int len = min(q.end - q.begin, K - 1);
     float w[CONV_CAUSAL_MAX_K], row[2 * CONV_CAUSAL_MAX_K], d[CONV_CAUSAL_MAX_K];
     for (int j = 0; j < K; ++j) w[j] = to_f32<T>(static_cast<const T*>(a.w)[static_cast<long long>(c) * K + j]);
     // row[j]: the window's rows, then the first tokens
-    for (int j = 0; j < K - 1 + len; ++j) {
-      float v[1];
-      row_or_window<T, 1, Q8>(v, a, n, q, q.begin + j - (K - 1), c);
-      row[j] = v[0];
-    }
+    for (int j = 0; j < K - 1 + len; ++j) row[j] = row_or_window<T, 1, Q8>(a, n, q, q.begin + j - (K - 1), c, 1)[0];
     for (int m = 0; m < K - 1; ++m) d[m] = 0.f;
     for (int p = 0; p < len; ++p) {
       const long long t = q.begin + p;
-      float dz = to_f32<T>(static_cast<const T*>(a.dy)[n * a.dy_batch + t * a.dy_token + c]);
+      float dz = to_f32<T>(static_cast<const T*>(a.dy.p)[n * a.dy.batch + t * a.dy.token + c]);
       if (a.silu) {
         float z = a.bias ? to_f32<T>(static_cast<const T*>(a.bias)[c]) : 0.f;
         for (int j = 0; j < K; ++j) z = fmaf(w[j], row[p + j], z);
-        dz *= silu_slope(z);
+        dz *= silu_slope(Vf<1>{{z}})[0];
       }
       for (int j = 0; p + j < K - 1; ++j) d[p + j] = fmaf(w[j], dz, d[p + j]);
     }
@@ -417,45 +527,33 @@ __global__ void __launch_bounds__(kCausalStepThreads) conv_causal_step_kernel(co
     if (a.fill) store_zero<T, V>(y + static_cast<long long>(b) * a.C);
     return;
   }
-  CausalArgs f = {};
-  f.w = a.w;
-  f.bias = a.bias;
-  f.K = a.K;
-  float w[KT][V], bias[V], old[KT - 1][V];
-  load_filter<T, KT, V>(w, bias, f, c);
+  Vf<V> w[KT], bias, old[KT - 1];  // old[o]: the row o + 1 tokens ago
+  load_filter<T, KT, V>(w, bias, a.w, a.bias, a.K, c, V);
   T* window = static_cast<T*>(a.state) + static_cast<long long>(slot) * (a.K - 1) * a.C + c;
 #pragma unroll
   for (int o = 0; o < KT - 1; ++o)
     if (o < a.K - 1) {
       const Raw<T, V> raw = *reinterpret_cast<const Raw<T, V>*>(window + static_cast<long long>(a.K - 2 - o) * a.C);
-      unpack<T, V>(raw, old[o]);
+      unpack<T, V>(raw, old[o].v);
     }
   do {
-    float x[V], z[V];
-    unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.x) + b * a.xs + c), x);
-#pragma unroll
-    for (int k = 0; k < V; ++k) z[k] = fmaf(w[0][k], x[k], bias[k]);
+    Vf<V> x;
+    unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.x) + b * a.xs + c), x.v);
+    Vf<V> z = fma_v(w[0], x, bias);
 #pragma unroll
     for (int o = 1; o < KT; ++o)
-      if (o < a.K)
+      if (has_tap<KT>(o, a.K)) z = fma_v(w[o], old[o - 1], z);
 #pragma unroll
-        for (int k = 0; k < V; ++k) z[k] = fmaf(w[o][k], old[o - 1][k], z[k]);
-#pragma unroll
-    for (int o = KT - 2; o > 0; --o)
-#pragma unroll
-      for (int k = 0; k < V; ++k) old[o][k] = old[o - 1][k];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      old[0][k] = x[k];
-      if (a.silu) z[k] = z[k] * causal_sigmoid(z[k]);
-    }
-    store_vec<T, V>(y + static_cast<long long>(b) * a.C, z);
+    for (int o = KT - 2; o > 0; --o) old[o] = old[o - 1];
+    old[0] = x;
+    if (a.silu) z = mul_v(z, sigmoid_v(z));
+    store_vec<T, V>(y + static_cast<long long>(b) * a.C, z.v);
     if (!(others & 2)) break;
     for (++b; b < a.B && __ldg(a.index + b) != slot;) ++b;
   } while (b < a.B);
 #pragma unroll
   for (int o = 0; o < KT - 1; ++o)
-    if (o < a.K - 1) store_vec<T, V>(window + static_cast<long long>(a.K - 2 - o) * a.C, old[o]);
+    if (o < a.K - 1) store_vec<T, V>(window + static_cast<long long>(a.K - 2 - o) * a.C, old[o].v);
 }
 
 }  // namespace convfwd

@@ -11,13 +11,13 @@ long long state_rows(int N, long long L, bool packed) {
 }
 
 // Sets `in` and the bytes it spans (values, then scales) in s[0], s[1].
-int take_input(ScanIn& in, Span* s, const void* p, const unsigned char* scale, long long batch, long long token, int N,
+int take_input(SeqIn& in, Span* s, const void* p, const unsigned char* scale, long long batch, long long token, int N,
                long long L, int C, bool packed, int esize) {
   long long elems;
   if (!strided_extent(N, L, C, packed, batch, token, elems)) return CONV_EINVAL;
   if (elems > 0 && !p) return CONV_EINVAL;
   if (!scale && !aligned_to(p, esize)) return CONV_EALIGN;
-  in = ScanIn{p, scale, batch, token};
+  in = SeqIn{p, scale, batch, token};
   s[0] = span_of(p, scale ? elems : elems * esize);
   s[1] = scale ? span_of(scale, (packed ? 1LL : N) * L * ((C + ACT8_BLOCK - 1LL) / ACT8_BLOCK)) : Span{0, 0};
   return CONV_OK;
@@ -34,7 +34,7 @@ int cluster_of(int N, long long L, int C, bool packed, int tokens) {
   return s;
 }
 
-bool rows_take16(const ScanIn& in, bool packed, int esize) {
+bool rows_take16(const SeqIn& in, bool packed, int esize) {
   return rows_aligned(in.p, packed ? 0 : in.batch, in.token, in.scale ? 1 : esize, 16);
 }
 
@@ -72,7 +72,7 @@ cudaError_t grad_as(const ScanArgs& a, int& parts, cudaStream_t st) {
 template <typename T, bool PACKED>
 cudaError_t grad_by(const ScanArgs& a, int& parts, cudaStream_t st) {
   bool aligned = a.C % (16 / static_cast<int>(sizeof(T))) == 0;
-  for (const ScanIn* in : {&a.x, &a.r, &a.i, &a.dy})
+  for (const SeqIn* in : {&a.x, &a.r, &a.i, &a.dy})
     aligned = aligned && (!in->scale || a.C % 16 == 0) && rows_take16(*in, PACKED, sizeof(T));
   for (const void* out : {a.dx, a.dr, a.di}) aligned = aligned && aligned_to(out, 2 * sizeof(T));
   if (a.x.scale)
@@ -179,7 +179,7 @@ int gated_scan_grad(const void* x, const unsigned char* x_scale, const void* r, 
   if ((x_scale == nullptr) != (r_scale == nullptr) || (x_scale == nullptr) != (i_scale == nullptr))
     return CONV_EUNSUPPORTED;
   if (x_scale)  // checkpoints are contiguous
-    for (const ScanIn* in : {&a.x, &a.r, &a.i})
+    for (const SeqIn* in : {&a.x, &a.r, &a.i})
       if ((L > 1 && in->token != C) || (!packed && N > 1 && in->batch != L * C)) return CONV_EUNSUPPORTED;
   const long long rows = packed ? L : N * L, nc = static_cast<long long>(N) * C;
   if (!decay || !ddecay || (rows > 0 && (!dx || !dr || !di || !states))) return CONV_EINVAL;
@@ -244,7 +244,7 @@ int gated_scan_step(const void* x, const void* r, const void* i, const float* de
   if (B < 0 || slots < 0 || !seq_sizes_ok(1, B, C, true) || slots > kSeqMaxElems / C) return CONV_EINVAL;
   if (!index && B > slots) return CONV_EINVAL;
   const int es = elem_size(dtype);
-  ScanIn in;
+  SeqIn in;
   Span ins[8], outs[2];
   int rc = take_input(in, ins, x, nullptr, 0, x_token, 1, B, C, true, es);
   if (rc == CONV_OK) rc = take_input(in, ins + 2, r, nullptr, 0, r_token, 1, B, C, true, es);

@@ -19,7 +19,7 @@
 #include <cmath>
 
 #include "ptx.cuh"
-#include "seq_common.cuh"
+#include "seq_tile.cuh"
 
 namespace convfwd {
 
@@ -101,9 +101,10 @@ __device__ __forceinline__ GateValues<V> gate_values(const GateConsts& c, const 
     o.a[k] = near1 ? near_a[k] : far[k];
   }
   o.m = mul_v(E, fma_v(E, none, both<V>(c.two)));
-  if constexpr (IN_ROOT)
+  if constexpr (IN_ROOT) {
 #pragma unroll
     for (int k = 0; k < V; ++k) o.m[k] = sqrt_approx(o.m[k]);
+  }
   return o;
 }
 // m g x, and NaN where a gate is
@@ -140,14 +141,8 @@ __device__ __forceinline__ Vf<V> gate_input(Raw<T, V> raw) {
   return o;
 }
 
-struct ScanIn {  // a strided tensor, or a checkpoint
-  const void* p;
-  const unsigned char* scale;
-  long long batch, token;
-};
-
 struct ScanArgs {
-  ScanIn x, r, i, dy;
+  SeqIn x, r, i, dy;
   const float *decay, *h0, *dh_last;
   const int* cu;
   void *y, *dx, *dr, *di;
@@ -193,9 +188,10 @@ __device__ __forceinline__ ScanMap<V> no_map() {
 template <bool PACKED, int V>
 __device__ __forceinline__ Vf<V> follow(const ScanMap<V>& f, const Vf<V>& h) {
   Vf<V> o = fma_v(f.P, h, f.H);
-  if (PACKED)
+  if (PACKED) {
 #pragma unroll
     for (int k = 0; k < V; ++k) o[k] = f.P[k] < 0.f ? f.H[k] : o[k];
+  }
   return o;
 }
 // f, then g
@@ -204,9 +200,10 @@ __device__ __forceinline__ ScanMap<V> then(const ScanMap<V>& f, const ScanMap<V>
   ScanMap<V> o;
   o.H = follow<PACKED>(g, f.H);
   o.P = mul_v(f.P, g.P);
-  if (PACKED)
+  if (PACKED) {
 #pragma unroll
     for (int k = 0; k < V; ++k) o.P[k] = f.P[k] < 0.f || g.P[k] < 0.f ? -1.f : o.P[k];
+  }
   return o;
 }
 // f, then a token: h -> a h + u
@@ -267,16 +264,6 @@ __device__ __forceinline__ void put_state(float* h, long long s, int C, int c, i
 #pragma unroll
   for (int k = 0; k < V; ++k)
     if (k < width) h[s * C + c + k] = v[k];
-}
-template <typename T, int V, bool ALIGNED>
-__device__ __forceinline__ void put_row(T* p, int width, const Vf<V>& v) {
-  if constexpr (ALIGNED) {
-    store_vec<T, V>(p, v.v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-      if (k < width) p[k] = from_f32<T>(v[k]);
-  }
 }
 // What sequences without a token pass on: `from` (or zeros) into `to`.
 template <int V>
@@ -377,86 +364,6 @@ __device__ __forceinline__ Vf<V> scan_exchange(ScanShared<V>& sh, int b, int ord
   return before;
 }
 
-// ---- rows in shared memory ------------------------------------------------
-//
-// Each warp copies its own rows of the next turn there while it works on this
-// one: 16 bytes an instruction and no registers, and only the warp itself waits
-// for them.  Rows that are not 16-byte aligned (ALIGNED false) go element by
-// element through registers, at the end of a turn when these are free: 8192
-// rows of 333 channels take 49 us, against 103 beside the turn's own values.
-template <typename T, int STEPS>
-struct alignas(16) ScanTile {
-  T v[STEPS][64];
-};
-
-__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
-               : "memory");  // zeros where it is not
-}
-__device__ __forceinline__ void copies_done() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncwarp();
-}
-
-// Walks along an input, a warp's STEPS rows of 64 channels a turn, zeros outside
-// of it.  The address of the lane's first element moves on by addition.
-template <typename T, int STEPS, bool ALIGNED>
-struct TileWalk {
-  static constexpr int kPer = 16 / sizeof(T), kRow = 64 / kPer, kRows = 32 / kRow;  // elements a copy, copies a row, rows at once
-  const T* p;       // of the lane's first row and channel
-  long long token;  // elements from row to row
-
-  // from row t0 on; `width` channels from c0 on are there
-  __device__ __forceinline__ void start(const ScanIn& in, int n, long long t0, int c0) {
-    const int lane = threadIdx.x & 31;
-    token = in.token;
-    p = static_cast<const T*>(in.p) + n * in.batch + c0 + t0 * token;
-    if constexpr (ALIGNED) p += lane / kRow * token + lane % kRow * kPer;
-  }
-  // Copies the rows into `tile`: `rows` of them are there (any number: none
-  // below 1, all from STEPS on).  Whole warps, behind their last use of the tile.
-  __device__ __forceinline__ void load(ScanTile<T, STEPS>& tile, int rows, int width) const {
-    const int lane = threadIdx.x & 31;
-    if constexpr (ALIGNED) {
-      const int row = lane / kRow, col = lane % kRow * kPer;
-      const int mine = col < width ? rows - row : 0;
-      T* to = &tile.v[row][col];
-      const T* from = p;
-#pragma unroll
-      for (int j = 0; j < STEPS; j += kRows) {
-        copy16(to + j * 64, from, j < mine);
-        if (j + kRows < mine) from += kRows * token;  // never behind the last row
-      }
-    } else {
-      T v[STEPS][2];  // loaded together
-      const T* from = p + lane;
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j) {
-        v[j][0] = j < rows && lane < width ? from[0] : T(0.f);
-        v[j][1] = j < rows && lane + 32 < width ? from[32] : T(0.f);
-        from += token;
-      }
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j) tile.v[j][lane] = v[j][0], tile.v[j][lane + 32] = v[j][1];
-    }
-  }
-  __device__ __forceinline__ void next(long long span) { p += span * token; }
-};
-
-// Rows that are in no sequence leave the state exactly as it is: their gate r
-// becomes -infinity and everything else 0.  Whole warps; `used`: bit j is row j.
-template <typename T, int STEPS>
-__device__ __forceinline__ void void_rows(ScanTile<T, STEPS>& tile, unsigned used, T with) {
-  const int lane = threadIdx.x & 31;
-  for (int j = 0; j < STEPS; ++j)
-    if (!(used >> j & 1)) tile.v[j][lane] = tile.v[j][lane + 32] = with;
-}
-
-template <typename T, int STEPS>
-__device__ __forceinline__ Raw<T, 2> row_pair(const ScanTile<T, STEPS>& tile, int j, int lane) {
-  return *reinterpret_cast<const Raw<T, 2>*>(&tile.v[j][2 * lane]);
-}
-
 // Tokens of a warp in the forward pass: the maps of a turn cost as much however
 // many there are, but a and u of each stay in registers.
 constexpr int kForwardSteps = 16;
@@ -465,7 +372,7 @@ template <typename T>
 struct ForwardShared {
   ScanShared<2> maps;
   struct {
-    ScanTile<T, kForwardSteps> x, r, i;
+    RowTile<T, kForwardSteps> x, r, i;
   } warp[kScanWarps];
 };
 
@@ -587,9 +494,9 @@ struct GradRows {
 
 template <typename T, bool ALIGNED>
 struct GradRows<T, true, ALIGNED> {
-  using Tile = ScanTile<T, kScanSteps>;
-  using Tile8 = ScanTile<signed char, kScanSteps>;
-  static_assert(kScanSteps * 64 == 32 * 16, "16 bytes a lane");
+  using Tile = RowTile<T, kScanSteps>;
+  using Tile8 = RowTile<signed char, kScanSteps>;
+  static_assert(kScanSteps == 8, "expand8 takes 8 rows");
   long long at, block;  // the walk's first element and the lane's step: the three are laid out alike
   int xs, rs, is;       // the lane's steps' bytes
 
@@ -598,10 +505,10 @@ struct GradRows<T, true, ALIGNED> {
     at = (n * a.L + t0) * a.C + c0;
     block = (n * a.L + t0 + lane / 4) * ((a.C + ACT8_BLOCK - 1) / ACT8_BLOCK) + c0 / ACT8_BLOCK + lane % 4 / 2;
   }
-  __device__ __forceinline__ int load_one(const ScanArgs& a, const ScanIn& in, Tile& tile, int rows, int width) const {
+  __device__ __forceinline__ int load_one(const ScanArgs& a, const SeqIn& in, Tile& tile, int rows, int width) const {
     const int lane = threadIdx.x & 31;
     TileWalk<signed char, kScanSteps, ALIGNED> walk;
-    walk.start(ScanIn{static_cast<const signed char*>(in.p) + at, nullptr, 0, a.C}, 0, 0, 0);
+    walk.start(SeqIn{static_cast<const signed char*>(in.p) + at, nullptr, 0, a.C}, 0, 0, 0);
     walk.load(reinterpret_cast<Tile8&>(tile), rows, width);
     return lane / 4 < rows && lane % 4 / 2 * ACT8_BLOCK < width ? __ldg(in.scale + block) : 0;
   }
@@ -615,30 +522,11 @@ struct GradRows<T, true, ALIGNED> {
     at += span * a.C;
     block += span * ((a.C + ACT8_BLOCK - 1) / ACT8_BLOCK);
   }
-  static __device__ __forceinline__ void expand_one(Tile& tile, int byte) {
-    const int lane = threadIdx.x & 31;
-    const uint4 raw = reinterpret_cast<const uint4*>(&tile)[lane];
-    const float step = act8_step(static_cast<unsigned char>(byte));
-    __syncwarp();
-    T* to = &tile.v[lane / 4][lane % 4 * 16];
-    const unsigned words[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      // q + 128 as the last byte of 2^23: a conversion would take the special functions' pipe
-      const unsigned biased = words[q] ^ 0x80808080u;
-      Vf<4> v;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7650 + k));
-      v = mul_v(add_v(v, splat<4>(-8388736.f)), splat<4>(step));
-      store_vec<T, 4>(to + 4 * q, v.v);
-    }
-  }
   template <typename Tiles>
   __device__ __forceinline__ void expand(Tiles& t) const {
-    expand_one(t.r, rs);
-    expand_one(t.i, is);
-    expand_one(t.x, xs);
-    __syncwarp();
+    expand8(t.r, 0, rs);
+    expand8(t.i, 0, is);
+    expand8(t.x, 0, xs);
   }
 };
 
@@ -647,10 +535,10 @@ struct GradShared {
   ScanShared<2> maps;
   ScanMap<2> ahead[2][kScanWarps][32];  // the forward maps, within the CTA
   struct {
-    ScanTile<T, kScanSteps> x, dy;
+    RowTile<T, kScanSteps> x, dy;
     union {
       struct {
-        ScanTile<T, kScanSteps> r, i;
+        RowTile<T, kScanSteps> r, i;
       };
       float2 m[kScanSteps][32];  // m, once r and i are used
     };

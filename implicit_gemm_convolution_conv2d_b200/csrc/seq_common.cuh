@@ -206,6 +206,24 @@ __device__ __forceinline__ int same_slot(const int* __restrict__ index, int B, i
   return (__any_sync(0xffffffffu, earlier) ? 1 : 0) | (__any_sync(0xffffffffu, later) ? 2 : 0);
 }
 
+// The first `width` of V channels into a row of an output (all of them where rows
+// are ALIGNED).
+template <typename T, int V, bool ALIGNED>
+__device__ __forceinline__ void put_row(T* p, int width, const Vf<V>& v) {
+  if constexpr (ALIGNED) {
+    store_vec<T, V>(p, v.v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (k < width) p[k] = from_f32<T>(v[k]);
+  }
+}
+struct SeqIn {  // a strided input, or a checkpoint where it has scales
+  const void* p;
+  const unsigned char* scale;
+  long long batch, token;
+};
+
 // ---- host side ----------------------------------------------------------
 
 struct Span {  // the bytes from a buffer's first element to its last
