@@ -438,5 +438,7 @@ def __getattr__(name):
                 "gated_scan_step", "Act8", "act8_pack", "act8_unpack"):
         import importlib
         mod = importlib.import_module(".seq", __name__)
-        return mod if name == "seq" else getattr(mod, name)
+        found = mod if name == "seq" else getattr(mod, name)
+        globals()[name] = found
+        return found
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

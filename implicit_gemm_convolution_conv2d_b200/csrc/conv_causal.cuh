@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kCausalThreads) conv_causal_kernel(const __gri
 //
 // dw and dbias of the run's own tokens are summed per warp, the block's warps in
 // shared memory in order, and blocks by conv_causal_sum_kernel in order.
-constexpr int kGradTogether = 4;
+constexpr int kGradTogether = 8;
 
 template <typename T>
 struct CausalGradShared {

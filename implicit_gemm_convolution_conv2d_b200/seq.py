@@ -18,6 +18,7 @@ on the current stream or on ``stream``; what it allocates belongs to that stream
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -74,33 +75,16 @@ def _lib():
     return _fn
 
 
-class _On:
-    """The device and stream of a call: makes them current where they are not."""
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
-    __slots__ = ("device", "stream", "handle", "_guards")
 
-    def __init__(self, t, stream):
-        self.device, self.stream, self._guards = t.device, stream, ()
-
-    def __enter__(self):
-        if self.stream is not None:
-            guard = torch.cuda.stream(self.stream)
-            guard.__enter__()
-            self._guards = (guard,)
-            self.handle = self.stream.cuda_stream
-        else:
-            at = self.device.index
-            if at != torch.cuda.current_device():
-                guard = torch.cuda.device(self.device)
-                guard.__enter__()
-                self._guards = (guard,)
-            self.handle = torch._C._cuda_getCurrentRawStream(at)
-        return self
-
-    def __exit__(self, *exc):
-        for g in self._guards:
-            g.__exit__(*exc)
-        return False
+def _elsewhere(t, stream):
+    """A context that makes a call's stream, or its tensors' device, current; None where they are."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if t.get_device() != _current_device():
+        return torch.cuda.device(t.device)
+    return None
 
 
 def _code(dtype, what):
@@ -117,12 +101,13 @@ def _cuda(t, name, what):
         raise ValueError(f"{what} runs on CUDA tensors only ({name} is not one)")
 
 
-def _same_device(like, what, **others):
-    for name, t in others.items():
-        if t is None:
-            continue
-        _cuda(t, name, what)
-        if t.device != like.device:
+def _same_device(like, what, names, *tensors):
+    """Every tensor is on the device of `like`; `names` has their names, for the error."""
+    at = like.get_device()
+    for k, t in enumerate(tensors):
+        if t is not None and not (isinstance(t, torch.Tensor) and t.get_device() == at):
+            name = names.split()[k]
+            _cuda(t, name, what)
             raise ValueError(f"{what}: {name} is on {t.device}, x on {like.device}")
 
 
@@ -156,7 +141,7 @@ def _rows(t, packed):
 
 
 def _check(t, shape, dtype, name, what):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what}: {name} must be {dtype} of shape {tuple(shape)}, not {t.dtype} of {tuple(t.shape)}")
 
 
@@ -178,6 +163,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace(name, *sizes):
+    """Bytes of workspace for these sizes, of which it is a function alone."""
+    out = ctypes.c_ulonglong()
+    _raise(_lib()[name](*sizes, ctypes.byref(out)), name)
+    return out.value
+
+
 def _raise(rc, what):
     if rc:
         raise ConvError(rc, what)
@@ -187,7 +180,7 @@ def _saved(v, what, name):
     """(values, scales or None, dtype) of an activation or its checkpoint."""
     if isinstance(v, Act8):
         _cuda(v.q, name, what)
-        _same_device(v.q, what, scale=v.scale)
+        _same_device(v.q, what, "scale", v.scale)
         blocks = (v.q.shape[-1] + ACT8_BLOCK - 1) // ACT8_BLOCK if v.q.dim() else 0
         _check(v.q, v.q.shape, torch.int8, f"{name}.q", what)
         _check(v.scale, (*v.q.shape[:-1], blocks), torch.uint8, f"{name}.scale", what)
@@ -210,14 +203,18 @@ def act8_pack(x, *, stream=None) -> Act8:
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError(f"{what}: x must be [..., C]")
     C = x.shape[-1]
-    with _On(x, stream) as on:
-        if x.dim() != 2 or x.stride(1) != 1 and C > 1:
-            x = x.contiguous()
-        rows = x.numel() // C
-        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-        scale = torch.empty((*x.shape[:-1], (C + ACT8_BLOCK - 1) // ACT8_BLOCK), dtype=torch.uint8, device=x.device)
-        _raise(_lib()["act8_pack"](x.data_ptr(), q.data_ptr(), scale.data_ptr(), rows, C,
-                                   x.stride(0) if x.dim() == 2 else C, code, on.handle), what)
+    there = _elsewhere(x, stream)
+    if there is not None:
+        with there:
+            return act8_pack(x)
+    stream = _raw_stream(x.get_device())
+    if x.dim() != 2 or x.stride(1) != 1 and C > 1:
+        x = x.contiguous()
+    rows = x.numel() // C
+    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    scale = torch.empty((*x.shape[:-1], (C + ACT8_BLOCK - 1) // ACT8_BLOCK), dtype=torch.uint8, device=x.device)
+    _raise(_lib()["act8_pack"](x.data_ptr(), q.data_ptr(), scale.data_ptr(), rows, C,
+                               x.stride(0) if x.dim() == 2 else C, code, stream), what)
     return Act8(q, scale, x.dtype)
 
 
@@ -229,15 +226,19 @@ def act8_unpack(p: Act8, *, out=None, stream=None):
     q, scale, dtype = _saved(p, what, "p")
     code = _code(dtype, what)
     C = q.shape[-1]
-    _same_device(q, what, out=out)
-    with _On(q, stream) as on:
-        if out is None:
-            out = torch.empty(q.shape, dtype=dtype, device=q.device)
-        else:
-            _check_out(out, q.shape, dtype, "out", what)
-        q, scale = q.contiguous(), scale.contiguous()
-        _raise(_lib()["act8_unpack"](q.data_ptr(), scale.data_ptr(), out.data_ptr(), q.numel() // C, C, code,
-                                     on.handle), what)
+    _same_device(q, what, "out", out)
+    there = _elsewhere(q, stream)
+    if there is not None:
+        with there:
+            return act8_unpack(p, out=out)
+    stream = _raw_stream(q.get_device())
+    if out is None:
+        out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    else:
+        _check_out(out, q.shape, dtype, "out", what)
+    q, scale = q.contiguous(), scale.contiguous()
+    _raise(_lib()["act8_unpack"](q.data_ptr(), scale.data_ptr(), out.data_ptr(), q.numel() // C, C, code,
+                                 stream), what)
     return out
 
 
@@ -265,22 +266,27 @@ def conv_causal(x, w, bias=None, *, activation=None, state=None, cu_seqlens=None
     each sequence)."""
     what = "conv_causal"
     _cuda(x, "x", what)
-    _same_device(x, what, w=w, bias=bias, state=state, cu_seqlens=cu_seqlens, out=out)
+    _same_device(x, what, "w bias state cu_seqlens out", w, bias, state, cu_seqlens, out)
     code = _code(x.dtype, what)
     N, L, C = _extents(x, cu_seqlens, what)
-    with _On(x, stream) as on:
-        w, bias, K = _filter(x.dtype, C, w, bias, activation, what)
-        state = _optional(state, (N, K - 1, C), x.dtype, "state", what)
-        fill = out is None
-        if fill:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _check_out(out, x.shape, x.dtype, "out", what)
-        left = torch.empty((N, K - 1, C), dtype=x.dtype, device=x.device) if return_state else None
-        x, xb, xt = _rows(x, cu_seqlens is not None)
-        _raise(_lib()["conv_causal"](x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(state), _ptr(cu_seqlens),
-                                     out.data_ptr(), _ptr(left), N, L, C, K, xb, xt, _ACT[activation], fill, code,
-                                     on.handle), what)
+    there = _elsewhere(x, stream)
+    if there is not None:
+        with there:
+            return conv_causal(x, w, bias, activation=activation, state=state, cu_seqlens=cu_seqlens,
+                               return_state=return_state, out=out)
+    stream = _raw_stream(x.get_device())
+    w, bias, K = _filter(x.dtype, C, w, bias, activation, what)
+    state = _optional(state, (N, K - 1, C), x.dtype, "state", what)
+    fill = out is None
+    if fill:
+        out = x.new_empty(x.shape)
+    else:
+        _check_out(out, x.shape, x.dtype, "out", what)
+    left = x.new_empty((N, K - 1, C)) if return_state else None
+    x, xb, xt = _rows(x, cu_seqlens is not None)
+    _raise(_lib()["conv_causal"](x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(state), _ptr(cu_seqlens),
+                                 out.data_ptr(), _ptr(left), N, L, C, K, xb, xt, _ACT[activation], fill, code,
+                                 stream), what)
     return (out, left) if return_state else out
 
 
@@ -293,30 +299,34 @@ def conv_causal_grad(x, w, dy, bias=None, *, activation=None, state=None, dstate
     where the forward pass had no bias or state."""
     what = "conv_causal_grad"
     xv, xs, dtype = _saved(x, what, "x")
-    _same_device(xv, what, w=w, dy=dy, bias=bias, state=state, dstate_out=dstate_out, cu_seqlens=cu_seqlens)
+    _same_device(xv, what, "w dy bias state dstate_out cu_seqlens", w, dy, bias, state, dstate_out, cu_seqlens)
     code = _code(dtype, what)
     N, L, C = _extents(xv, cu_seqlens, what)
     _check(dy, xv.shape, dtype, "dy", what)
     packed = cu_seqlens is not None
-    with _On(xv, stream) as on:
-        w, bias, K = _filter(dtype, C, w, bias, activation, what)
-        state = _optional(state, (N, K - 1, C), dtype, "state", what)
-        dstate_out = _optional(dstate_out, (N, K - 1, C), dtype, "dstate_out", what)
-        xv, xb, xt = _rows(xv, packed)
-        dy, yb, yt = _rows(dy, packed)
-        if xs is not None:
-            xs = xs.contiguous()
-        dx = torch.empty(dy.shape, dtype=dtype, device=dy.device)
-        dw = torch.empty((C, K), dtype=dtype, device=dy.device)
-        db = None if bias is None else torch.empty(C, dtype=dtype, device=dy.device)
-        ds = None if state is None else torch.empty((N, K - 1, C), dtype=dtype, device=dy.device)
-        need = ctypes.c_ulonglong()
-        _raise(_lib()["conv_causal_grad_workspace_size"](N, L, C, K, packed, ctypes.byref(need)), what)
-        work = torch.empty(need.value // 4, dtype=torch.float32, device=dy.device)
-        _raise(_lib()["conv_causal_grad"](xv.data_ptr(), _ptr(xs), w.data_ptr(), _ptr(bias), _ptr(state),
-                                          _ptr(cu_seqlens), dy.data_ptr(), _ptr(dstate_out), dx.data_ptr(),
-                                          dw.data_ptr(), _ptr(db), _ptr(ds), N, L, C, K, xb, xt, yb, yt,
-                                          _ACT[activation], True, code, work.data_ptr(), need.value, on.handle), what)
+    there = _elsewhere(xv, stream)
+    if there is not None:
+        with there:
+            return conv_causal_grad(x, w, dy, bias, activation=activation, state=state, dstate_out=dstate_out,
+                                    cu_seqlens=cu_seqlens)
+    stream = _raw_stream(xv.get_device())
+    w, bias, K = _filter(dtype, C, w, bias, activation, what)
+    state = _optional(state, (N, K - 1, C), dtype, "state", what)
+    dstate_out = _optional(dstate_out, (N, K - 1, C), dtype, "dstate_out", what)
+    xv, xb, xt = _rows(xv, packed)
+    dy, yb, yt = _rows(dy, packed)
+    if xs is not None:
+        xs = xs.contiguous()
+    dx = dy.new_empty(dy.shape)
+    dw = dy.new_empty((C, K))
+    db = None if bias is None else dy.new_empty(C)
+    ds = None if state is None else dy.new_empty((N, K - 1, C))
+    need = _workspace("conv_causal_grad_workspace_size", N, L, C, K, packed)
+    work = dy.new_empty(need // 4, dtype=torch.float32)
+    _raise(_lib()["conv_causal_grad"](xv.data_ptr(), _ptr(xs), w.data_ptr(), _ptr(bias), _ptr(state),
+                                      _ptr(cu_seqlens), dy.data_ptr(), _ptr(dstate_out), dx.data_ptr(),
+                                      dw.data_ptr(), _ptr(db), _ptr(ds), N, L, C, K, xb, xt, yb, yt,
+                                      _ACT[activation], True, code, work.data_ptr(), need, stream), what)
     return dx, dw, db, ds
 
 
@@ -342,22 +352,26 @@ def conv_causal_step(x, w, state, bias=None, *, activation=None, index=None, out
     sequence's consecutive tokens."""
     what = "conv_causal_step"
     _cuda(x, "x", what)
-    _same_device(x, what, w=w, state=state, bias=bias, index=index, out=out)
+    _same_device(x, what, "w state bias index out", w, state, bias, index, out)
     code = _code(x.dtype, what)
     B, C = _step_rows(x, state.shape[0] if state.dim() == 3 else 0, index, what), x.shape[1]
-    with _On(x, stream) as on:
-        w, bias, K = _filter(x.dtype, C, w, bias, activation, what)
-        slots = state.shape[0]
-        _check_out(state, (slots, K - 1, C), x.dtype, "state", what)
-        fill = out is None
-        if fill:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _check_out(out, x.shape, x.dtype, "out", what)
-        x, _, xt = _rows(x, True)
-        _raise(_lib()["conv_causal_step"](x.data_ptr(), w.data_ptr(), _ptr(bias), state.data_ptr(), _ptr(index),
-                                          out.data_ptr(), B, slots, C, K, xt, _ACT[activation], fill, code,
-                                          on.handle), what)
+    there = _elsewhere(x, stream)
+    if there is not None:
+        with there:
+            return conv_causal_step(x, w, state, bias, activation=activation, index=index, out=out)
+    stream = _raw_stream(x.get_device())
+    w, bias, K = _filter(x.dtype, C, w, bias, activation, what)
+    slots = state.shape[0]
+    _check_out(state, (slots, K - 1, C), x.dtype, "state", what)
+    fill = out is None
+    if fill:
+        out = x.new_empty(x.shape)
+    else:
+        _check_out(out, x.shape, x.dtype, "out", what)
+    x, _, xt = _rows(x, True)
+    _raise(_lib()["conv_causal_step"](x.data_ptr(), w.data_ptr(), _ptr(bias), state.data_ptr(), _ptr(index),
+                                      out.data_ptr(), B, slots, C, K, xt, _ACT[activation], fill, code,
+                                      stream), what)
     return out
 
 
@@ -379,30 +393,34 @@ def gated_scan(x, r, i, decay, *, h0=None, cu_seqlens=None, save_states=False, o
     front of every 64th token, fp32 [N, ceil(L / 64), C] (packed: N = 1)."""
     what = "gated_scan"
     _cuda(x, "x", what)
-    _same_device(x, what, r=r, i=i, decay=decay, h0=h0, cu_seqlens=cu_seqlens, out=out)
+    _same_device(x, what, "r i decay h0 cu_seqlens out", r, i, decay, h0, cu_seqlens, out)
     code = _code(x.dtype, what)
     N, L, C = _extents(x, cu_seqlens, what)
     _check(r, x.shape, x.dtype, "r", what)
     _check(i, x.shape, x.dtype, "i", what)
     packed = cu_seqlens is not None
-    with _On(x, stream) as on:
-        decay = _decay(decay, C, what)
-        h0 = _optional(h0, (N, C), torch.float32, "h0", what)
-        fill = out is None
-        if fill:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _check_out(out, x.shape, x.dtype, "out", what)
-        last = torch.empty((N, C), dtype=torch.float32, device=x.device)
-        states = None
-        if save_states:
-            states = torch.empty((1 if packed else N, (L + 63) // 64, C), dtype=torch.float32, device=x.device)
-        x, xb, xt = _rows(x, packed)
-        r, rb, rt = _rows(r, packed)
-        i, ib, it = _rows(i, packed)
-        _raise(_lib()["gated_scan"](x.data_ptr(), r.data_ptr(), i.data_ptr(), decay.data_ptr(), _ptr(h0),
-                                    _ptr(cu_seqlens), out.data_ptr(), last.data_ptr(), _ptr(states), N, L, C, xb, xt,
-                                    rb, rt, ib, it, fill, code, on.handle), what)
+    there = _elsewhere(x, stream)
+    if there is not None:
+        with there:
+            return gated_scan(x, r, i, decay, h0=h0, cu_seqlens=cu_seqlens, save_states=save_states, out=out)
+    stream = _raw_stream(x.get_device())
+    decay = _decay(decay, C, what)
+    h0 = _optional(h0, (N, C), torch.float32, "h0", what)
+    fill = out is None
+    if fill:
+        out = x.new_empty(x.shape)
+    else:
+        _check_out(out, x.shape, x.dtype, "out", what)
+    last = decay.new_empty((N, C))
+    states = None
+    if save_states:
+        states = decay.new_empty((1 if packed else N, (L + 63) // 64, C))
+    x, xb, xt = _rows(x, packed)
+    r, rb, rt = _rows(r, packed)
+    i, ib, it = _rows(i, packed)
+    _raise(_lib()["gated_scan"](x.data_ptr(), r.data_ptr(), i.data_ptr(), decay.data_ptr(), _ptr(h0),
+                                _ptr(cu_seqlens), out.data_ptr(), last.data_ptr(), _ptr(states), N, L, C, xb, xt,
+                                rb, rt, ib, it, fill, code, stream), what)
     return (out, last, states) if save_states else (out, last)
 
 
@@ -416,39 +434,41 @@ def gated_scan_grad(x, r, i, decay, dy, states, *, h0=None, dh_last=None, cu_seq
     xv, xs, dtype = _saved(x, what, "x")
     rv, rs, rd = _saved(r, what, "r")
     iv, is_, idt = _saved(i, what, "i")
-    _same_device(xv, what, r=rv, i=iv, decay=decay, dy=dy, states=states, h0=h0, dh_last=dh_last,
-                 cu_seqlens=cu_seqlens)
+    _same_device(xv, what, "r i decay dy states h0 dh_last cu_seqlens", rv, iv, decay, dy, states, h0, dh_last, cu_seqlens)
     code = _code(dtype, what)
     N, L, C = _extents(xv, cu_seqlens, what)
     for name, t, d in (("r", rv, rd), ("i", iv, idt), ("dy", dy, dy.dtype)):
         if t.shape != xv.shape or d != dtype:
             raise ValueError(f"{what}: {name} must be {dtype} of shape {tuple(xv.shape)}")
     packed = cu_seqlens is not None
-    with _On(xv, stream) as on:
-        if not (xs is None) == (rs is None) == (is_ is None):  # a mixture: the kernel takes all or none in 8 bits
-            xv, rv, iv = (act8_unpack(v) if isinstance(v, Act8) else v for v in (x, r, i))
-            xs = rs = is_ = None
-        decay = _decay(decay, C, what)
-        states = _optional(states, (1 if packed else N, (L + 63) // 64, C), torch.float32, "states", what)
-        h0 = _optional(h0, (N, C), torch.float32, "h0", what)
-        dh_last = _optional(dh_last, (N, C), torch.float32, "dh_last", what)
-        if xs is not None:
-            xv, rv, iv, xs, rs, is_ = (t.contiguous() for t in (xv, rv, iv, xs, rs, is_))
-        xv, xb, xt = _rows(xv, packed)
-        rv, rb, rt = _rows(rv, packed)
-        iv, ib, it = _rows(iv, packed)
-        dy, yb, yt = _rows(dy, packed)
-        dx, dr, di = (torch.empty(dy.shape, dtype=dtype, device=dy.device) for _ in range(3))
-        ddecay = torch.empty(C, dtype=torch.float32, device=dy.device)
-        dh0 = None if h0 is None else torch.empty((N, C), dtype=torch.float32, device=dy.device)
-        need = ctypes.c_ulonglong()
-        _raise(_lib()["gated_scan_grad_workspace_size"](N, L, C, packed, ctypes.byref(need)), what)
-        work = torch.empty((need.value + 3) // 4, dtype=torch.float32, device=dy.device)
-        _raise(_lib()["gated_scan_grad"](xv.data_ptr(), _ptr(xs), rv.data_ptr(), _ptr(rs), iv.data_ptr(), _ptr(is_),
-                                         decay.data_ptr(), _ptr(states), _ptr(h0), _ptr(cu_seqlens), dy.data_ptr(),
-                                         _ptr(dh_last), dx.data_ptr(), dr.data_ptr(), di.data_ptr(),
-                                         ddecay.data_ptr(), _ptr(dh0), N, L, C, xb, xt, rb, rt, ib, it, yb, yt, True,
-                                         code, work.data_ptr(), need.value, on.handle), what)
+    there = _elsewhere(xv, stream)
+    if there is not None:
+        with there:
+            return gated_scan_grad(x, r, i, decay, dy, states, h0=h0, dh_last=dh_last, cu_seqlens=cu_seqlens)
+    stream = _raw_stream(xv.get_device())
+    if not (xs is None) == (rs is None) == (is_ is None):  # a mixture: the kernel takes all or none in 8 bits
+        xv, rv, iv = (act8_unpack(v) if isinstance(v, Act8) else v for v in (x, r, i))
+        xs = rs = is_ = None
+    decay = _decay(decay, C, what)
+    states = _optional(states, (1 if packed else N, (L + 63) // 64, C), torch.float32, "states", what)
+    h0 = _optional(h0, (N, C), torch.float32, "h0", what)
+    dh_last = _optional(dh_last, (N, C), torch.float32, "dh_last", what)
+    if xs is not None:
+        xv, rv, iv, xs, rs, is_ = (t.contiguous() for t in (xv, rv, iv, xs, rs, is_))
+    xv, xb, xt = _rows(xv, packed)
+    rv, rb, rt = _rows(rv, packed)
+    iv, ib, it = _rows(iv, packed)
+    dy, yb, yt = _rows(dy, packed)
+    dx, dr, di = (dy.new_empty(dy.shape) for _ in range(3))
+    ddecay = decay.new_empty(C)
+    dh0 = None if h0 is None else decay.new_empty((N, C))
+    need = _workspace("gated_scan_grad_workspace_size", N, L, C, packed)
+    work = decay.new_empty(need // 4)
+    _raise(_lib()["gated_scan_grad"](xv.data_ptr(), _ptr(xs), rv.data_ptr(), _ptr(rs), iv.data_ptr(), _ptr(is_),
+                                     decay.data_ptr(), _ptr(states), _ptr(h0), _ptr(cu_seqlens), dy.data_ptr(),
+                                     _ptr(dh_last), dx.data_ptr(), dr.data_ptr(), di.data_ptr(),
+                                     ddecay.data_ptr(), _ptr(dh0), N, L, C, xb, xt, rb, rt, ib, it, yb, yt, True,
+                                     code, work.data_ptr(), need, stream), what)
     return dx, dr, di, ddecay, dh0
 
 
@@ -459,24 +479,28 @@ def gated_scan_step(x, r, i, decay, h, *, index=None, out=None, stream=None):
     rows and rows naming one slot as for conv_causal_step."""
     what = "gated_scan_step"
     _cuda(x, "x", what)
-    _same_device(x, what, r=r, i=i, decay=decay, h=h, index=index, out=out)
+    _same_device(x, what, "r i decay h index out", r, i, decay, h, index, out)
     code = _code(x.dtype, what)
     B, C = _step_rows(x, h.shape[0] if h.dim() == 2 else 0, index, what), x.shape[1]
     _check(r, x.shape, x.dtype, "r", what)
     _check(i, x.shape, x.dtype, "i", what)
     slots = h.shape[0]
     _check_out(h, (slots, C), torch.float32, "h", what)
-    with _On(x, stream) as on:
-        decay = _decay(decay, C, what)
-        fill = out is None
-        if fill:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _check_out(out, x.shape, x.dtype, "out", what)
-        x, _, xt = _rows(x, True)
-        r, _, rt = _rows(r, True)
-        i, _, it = _rows(i, True)
-        _raise(_lib()["gated_scan_step"](x.data_ptr(), r.data_ptr(), i.data_ptr(), decay.data_ptr(), h.data_ptr(),
-                                         _ptr(index), out.data_ptr(), B, slots, C, xt, rt, it, fill, code, on.handle),
-               what)
+    there = _elsewhere(x, stream)
+    if there is not None:
+        with there:
+            return gated_scan_step(x, r, i, decay, h, index=index, out=out)
+    stream = _raw_stream(x.get_device())
+    decay = _decay(decay, C, what)
+    fill = out is None
+    if fill:
+        out = x.new_empty(x.shape)
+    else:
+        _check_out(out, x.shape, x.dtype, "out", what)
+    x, _, xt = _rows(x, True)
+    r, _, rt = _rows(r, True)
+    i, _, it = _rows(i, True)
+    _raise(_lib()["gated_scan_step"](x.data_ptr(), r.data_ptr(), i.data_ptr(), decay.data_ptr(), h.data_ptr(),
+                                     _ptr(index), out.data_ptr(), B, slots, C, xt, rt, it, fill, code, stream),
+           what)
     return out
