@@ -81,10 +81,17 @@ _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurre
 def _elsewhere(t, stream):
     """A context that makes a call's stream, or its tensors' device, current; None where they are."""
     if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
         return torch.cuda.stream(stream)
     if t.get_device() != _current_device():
         return torch.cuda.device(t.device)
     return None
+
+
+def _new_like(t):
+    """A contiguous tensor of t's shape and type (empty_like, where it gives that, costs the host least)."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _code(dtype, what):
@@ -211,8 +218,8 @@ def act8_pack(x, *, stream=None) -> Act8:
     if x.dim() != 2 or x.stride(1) != 1 and C > 1:
         x = x.contiguous()
     rows = x.numel() // C
-    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-    scale = torch.empty((*x.shape[:-1], (C + ACT8_BLOCK - 1) // ACT8_BLOCK), dtype=torch.uint8, device=x.device)
+    q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
+    scale = x.new_empty((*x.shape[:-1], (C + ACT8_BLOCK - 1) // ACT8_BLOCK), dtype=torch.uint8)
     _raise(_lib()["act8_pack"](x.data_ptr(), q.data_ptr(), scale.data_ptr(), rows, C,
                                x.stride(0) if x.dim() == 2 else C, code, stream), what)
     return Act8(q, scale, x.dtype)
@@ -233,7 +240,7 @@ def act8_unpack(p: Act8, *, out=None, stream=None):
             return act8_unpack(p, out=out)
     stream = _raw_stream(q.get_device())
     if out is None:
-        out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        out = torch.empty_like(q, dtype=dtype, memory_format=torch.contiguous_format)
     else:
         _check_out(out, q.shape, dtype, "out", what)
     q, scale = q.contiguous(), scale.contiguous()
@@ -279,7 +286,7 @@ def conv_causal(x, w, bias=None, *, activation=None, state=None, cu_seqlens=None
     state = _optional(state, (N, K - 1, C), x.dtype, "state", what)
     fill = out is None
     if fill:
-        out = x.new_empty(x.shape)
+        out = _new_like(x)
     else:
         _check_out(out, x.shape, x.dtype, "out", what)
     left = x.new_empty((N, K - 1, C)) if return_state else None
@@ -317,7 +324,7 @@ def conv_causal_grad(x, w, dy, bias=None, *, activation=None, state=None, dstate
     dy, yb, yt = _rows(dy, packed)
     if xs is not None:
         xs = xs.contiguous()
-    dx = dy.new_empty(dy.shape)
+    dx = _new_like(dy)
     dw = dy.new_empty((C, K))
     db = None if bias is None else dy.new_empty(C)
     ds = None if state is None else dy.new_empty((N, K - 1, C))
@@ -365,7 +372,7 @@ def conv_causal_step(x, w, state, bias=None, *, activation=None, index=None, out
     _check_out(state, (slots, K - 1, C), x.dtype, "state", what)
     fill = out is None
     if fill:
-        out = x.new_empty(x.shape)
+        out = _new_like(x)
     else:
         _check_out(out, x.shape, x.dtype, "out", what)
     x, _, xt = _rows(x, True)
@@ -408,7 +415,7 @@ def gated_scan(x, r, i, decay, *, h0=None, cu_seqlens=None, save_states=False, o
     h0 = _optional(h0, (N, C), torch.float32, "h0", what)
     fill = out is None
     if fill:
-        out = x.new_empty(x.shape)
+        out = _new_like(x)
     else:
         _check_out(out, x.shape, x.dtype, "out", what)
     last = decay.new_empty((N, C))
@@ -459,7 +466,7 @@ def gated_scan_grad(x, r, i, decay, dy, states, *, h0=None, dh_last=None, cu_seq
     rv, rb, rt = _rows(rv, packed)
     iv, ib, it = _rows(iv, packed)
     dy, yb, yt = _rows(dy, packed)
-    dx, dr, di = (dy.new_empty(dy.shape) for _ in range(3))
+    dx, dr, di = _new_like(dy), _new_like(dy), _new_like(dy)
     ddecay = decay.new_empty(C)
     dh0 = None if h0 is None else decay.new_empty((N, C))
     need = _workspace("gated_scan_grad_workspace_size", N, L, C, packed)
@@ -494,7 +501,7 @@ def gated_scan_step(x, r, i, decay, h, *, index=None, out=None, stream=None):
     decay = _decay(decay, C, what)
     fill = out is None
     if fill:
-        out = x.new_empty(x.shape)
+        out = _new_like(x)
     else:
         _check_out(out, x.shape, x.dtype, "out", what)
     x, _, xt = _rows(x, True)
