@@ -18,7 +18,7 @@ int pack(const void* x, signed char* q, unsigned char* scale, long long rows, in
     e = launch_pdl(act8_pack_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kAct8Threads), 0, st, 1, xt, q,
                    scale, rows, C, x_row);
   } else {
-    const long long blocks = std::min<long long>((rows * nblk + 7) / 8, 16LL * sm_count());
+    const long long blocks = std::min<long long>((rows * ((nblk + kAct8Unroll - 1) / kAct8Unroll) + 7) / 8, 16LL * sm_count());
     e = launch_pdl(act8_pack_any_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kAct8Threads), 0, st, 1, xt, q,
                    scale, rows, C, x_row);
   }
@@ -36,7 +36,9 @@ int unpack_rows(const signed char* q, const unsigned char* scale, void* y, long 
     e = launch_pdl(act8_unpack_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kAct8Threads), 0, st, 1, q, scale,
                    yt, rows, C);
   } else {
-    const long long blocks = std::min<long long>((rows * C + kAct8Threads - 1) / kAct8Threads, 16LL * sm_count());
+    const long long nblk = (C + ACT8_BLOCK - 1) / ACT8_BLOCK;
+    const long long blocks =
+        std::min<long long>((rows * ((nblk + kAct8Unroll - 1) / kAct8Unroll) + 7) / 8, 16LL * sm_count());
     e = launch_pdl(act8_unpack_any_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kAct8Threads), 0, st, 1, q,
                    scale, yt, rows, C);
   }
