@@ -52,6 +52,12 @@ long long run_blocks(int N, long long L, int run, bool packed) {
   return std::max<long long>(1, (runs + kCausalWarps - 1) / kCausalWarps);
 }
 
+// Channels along x; the blocks along y, and along z where they pass y's limit.
+dim3 run_grid(int C, long long blocks) {
+  const long long y = std::min<long long>(blocks, 65535);
+  return dim3((C + 63) / 64, static_cast<unsigned>(y), static_cast<unsigned>((blocks + y - 1) / y));
+}
+
 bool aligned_rows(const SeqIn& in, bool packed, int C, int esize) {
   const int e = in.scale ? 1 : esize;
   return C % (16 / e) == 0 && rows_aligned(in.p, packed ? 0 : in.batch, in.token, e, 16);
@@ -111,8 +117,9 @@ int conv_causal(const void* x, const void* w, const void* bias, const void* stat
   a.run = run_length(rows, C, 24);
   a.runs = static_cast<int>((L + a.run - 1) / a.run);
   const long long by = run_blocks(N, L, a.run, packed);
-  if (by > 65535) return CONV_EUNSUPPORTED;
-  const dim3 grid((C + 63) / 64, static_cast<unsigned>(by));
+  if (by > 0x7fffffffLL) return CONV_EUNSUPPORTED;
+  a.blocks = static_cast<int>(by);
+  const dim3 grid = run_grid(C, by);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = by_type_and_taps(dtype, K, [&](auto t, auto kt) {
     using T = typename decltype(t)::type;
@@ -174,8 +181,9 @@ int conv_causal_grad(const void* x, const unsigned char* x_scale, const void* w,
   a.run = grad_run(N, L, C, packed);
   a.runs = static_cast<int>((L + a.run - 1) / a.run);
   const long long by = run_blocks(N, L, a.run, packed);
-  if (by > 65535) return CONV_EUNSUPPORTED;
-  const dim3 grid((C + 63) / 64, static_cast<unsigned>(by));
+  if (by > 0x7fffffffLL) return CONV_EUNSUPPORTED;
+  a.blocks = static_cast<int>(by);
+  const dim3 grid = run_grid(C, by);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = by_type_and_taps(dtype, K, [&](auto t, auto kt) {
     using T = typename decltype(t)::type;

@@ -28,6 +28,7 @@ struct CausalArgs {
   int L;      // tokens of a sequence (packed: all rows)
   int run;    // tokens of a warp's run
   int runs;   // runs of a sequence (packed: of all rows)
+  int blocks; // of kCausalWarps runs
 };
 
 // The sequence of a token, as the warps walk along it.
@@ -140,11 +141,11 @@ __global__ void __launch_bounds__(kCausalThreads) conv_causal_kernel(const __gri
   const int c0 = blockIdx.x * 64, c = c0 + lane * V, there = a.C - c0;
   const int width = min(V, a.C - c);
   const bool in = width > 0;
-  const long long job = static_cast<long long>(blockIdx.y) * kCausalWarps + warp;
+  const long long block = static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y, job = block * kCausalWarps + warp;
   T* state_out = static_cast<T*>(a.state_out);
   if (state_out && in) {
     // sequences without a token leave their window as it was
-    for (long long s = job; s < a.N; s += static_cast<long long>(gridDim.y) * kCausalWarps) {
+    for (long long s = job; s < a.N; s += static_cast<long long>(gridDim.y) * gridDim.z * kCausalWarps) {
       if (a.cu ? __ldg(a.cu + s) < __ldg(a.cu + s + 1) : a.L > 0) continue;
       const SeqAt q{static_cast<int>(s), 0, 0};
       for (int j = 0; j < a.K - 1; ++j)
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kCausalThreads, 2) conv_causal_grad_kernel(con
   const int c0 = blockIdx.x * 64, c = c0 + lane * V, there = a.C - c0;
   const int width = min(V, a.C - c);
   const bool in = width > 0;
-  const long long job = static_cast<long long>(blockIdx.y) * kCausalWarps + warp;
+  const long long block = static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y, job = block * kCausalWarps + warp;
   GradRegs<T, KT, Q8> k;
   k.db = splat<V>(0.f);
 #pragma unroll
@@ -426,11 +427,11 @@ __global__ void __launch_bounds__(kCausalThreads, 2) conv_causal_grad_kernel(con
     sums[warp][lane] = o < KT ? k.dw[o < KT ? o : 0] : k.db;
     __syncthreads();
     const int row = o < KT ? a.K - 1 - o : a.K;
-    if (warp == 0 && in) {
+    if (warp == 0 && in && block < a.blocks) {
       Vf<V> sum = sums[0][lane];
 #pragma unroll
       for (int r = 1; r < kCausalWarps; ++r) sum = add_v(sum, sums[r][lane]);
-      float* part = a.part + (static_cast<long long>(blockIdx.y) * (a.K + 1) + row) * a.C + c;
+      float* part = a.part + (block * (a.K + 1) + row) * a.C + c;
 #pragma unroll
       for (int e = 0; e < V; ++e)
         if (e < width) part[e] = sum[e];

@@ -34,6 +34,12 @@ int cluster_of(int N, long long L, int C, bool packed, int tokens) {
   return s;
 }
 
+// Clusters along x; the batch along y, and along z where it passes y's limit.
+dim3 scan_grid(const ScanArgs& a, int ctas, bool packed) {
+  const unsigned n = packed ? 1 : a.N, y = std::min(n, 65535u);
+  return dim3((a.C + 63) / 64 * ctas, y, (n + y - 1) / y);
+}
+
 bool rows_take16(const SeqIn& in, bool packed, int esize) {
   return rows_aligned(in.p, packed ? 0 : in.batch, in.token, in.scale ? 1 : esize, 16);
 }
@@ -41,7 +47,7 @@ bool rows_take16(const SeqIn& in, bool packed, int esize) {
 template <typename T, bool PACKED, bool ALIGNED>
 cudaError_t forward_as(const ScanArgs& a, cudaStream_t st) {
   const int s = cluster_of(a.N, a.L, a.C, PACKED, kScanWarps * kForwardSteps);
-  const dim3 grid((a.C + 63) / 64 * s, PACKED ? 1 : a.N);
+  const dim3 grid = scan_grid(a, s, PACKED);
   auto* k = gated_scan_kernel<T, PACKED, ALIGNED>;
   const size_t smem = sizeof(ForwardShared<T>);
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -61,8 +67,8 @@ cudaError_t launch_forward(const ScanArgs& a, cudaStream_t st) {
 template <typename T, bool PACKED, bool ALIGNED, bool Q8>
 cudaError_t grad_as(const ScanArgs& a, int& parts, cudaStream_t st) {
   const int s = cluster_of(a.N, a.L, a.C, PACKED, GATED_SCAN_STATE_EVERY);
-  const dim3 grid((a.C + 63) / 64 * s, PACKED ? 1 : a.N);
-  parts = s * static_cast<int>(grid.y);
+  const dim3 grid = scan_grid(a, s, PACKED);
+  parts = s * (PACKED ? 1 : a.N);
   auto* k = gated_scan_grad_kernel<T, PACKED, ALIGNED, Q8>;
   const size_t smem = sizeof(GradShared<T>);
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -108,7 +114,7 @@ int gated_scan(const void* x, const void* r, const void* i, const float* decay, 
                conv_stream_t stream) {
   if (!dtype_ok(dtype)) return CONV_EDTYPE;
   const bool packed = cu != nullptr;
-  if (!seq_sizes_ok(N, L, C, packed) || N > 65535) return CONV_EINVAL;
+  if (!seq_sizes_ok(N, L, C, packed)) return CONV_EINVAL;
   const int es = elem_size(dtype);
   ScanArgs a = {};
   Span ins[9], outs[3];
@@ -154,7 +160,8 @@ int gated_scan(const void* x, const void* r, const void* i, const float* decay, 
 
 int gated_scan_grad_workspace_size(int N, long long L, int C, int packed, unsigned long long* bytes) {
   if (!seq_sizes_ok(N, L, C, packed != 0) || !bytes) return CONV_EINVAL;
-  *bytes = 4ull * (packed ? 1 : N) * kScanMaxCluster * C;  // a row a CTA of a channel
+  // a row for each CTA that has a channel
+  *bytes = 4ull * (packed ? 1 : N) * cluster_of(N, L, C, packed != 0, GATED_SCAN_STATE_EVERY) * C;
   return CONV_OK;
 }
 
@@ -167,7 +174,7 @@ int gated_scan_grad(const void* x, const unsigned char* x_scale, const void* r, 
                     conv_stream_t stream) {
   if (!dtype_ok(dtype)) return CONV_EDTYPE;
   const bool packed = cu != nullptr;
-  if (!seq_sizes_ok(N, L, C, packed) || N > 65535) return CONV_EINVAL;
+  if (!seq_sizes_ok(N, L, C, packed)) return CONV_EINVAL;
   const int es = elem_size(dtype);
   ScanArgs a = {};
   Span ins[13], outs[6];
@@ -232,7 +239,7 @@ int gated_scan_grad(const void* x, const unsigned char* x_scale, const void* r, 
                                               : launch_grad<__nv_bfloat16>(a, parts, st);
     if (e != cudaSuccess) return CONV_ELAUNCH;
   }
-  const cudaError_t e = launch_pdl(gated_scan_sum_kernel, dim3((C + 63) / 64), dim3(64), 0, st, 1,
+  const cudaError_t e = launch_pdl(gated_scan_sum_kernel, dim3((C + 31) / 32), dim3(32, 8), 0, st, 1,
                                    static_cast<const float*>(a.part), ddecay, parts, C);
   return e == cudaSuccess ? CONV_OK : CONV_ELAUNCH;
 }

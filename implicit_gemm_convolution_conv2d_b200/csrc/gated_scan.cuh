@@ -155,8 +155,7 @@ struct ScanArgs {
 
 // ---- one pass over time --------------------------------------------------
 //
-// A warp owns 32 * V neighbouring channels and kSteps tokens in a row, kept in
-// registers; a CTA is kScanWarps warps, one behind the other in time; a cluster
+// A warp owns 64 neighbouring channels, two a lane, and a few tokens in a row; a CTA is kScanWarps warps, one behind the other in time; a cluster
 // is up to eight CTAs one behind the other, and walks along a sequence in turns
 // of as many tokens as it holds.  A segment of tokens is the map
 // h -> P h + H (P the product of its a's, H its own end state), so per turn the
@@ -385,7 +384,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const __gri
   ptx::pdl_wait_prev();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = cluster_rank(), ctas = cluster_size();
-  const int c0 = static_cast<int>(blockIdx.x / ctas) * 64, c = c0 + lane * V, n = blockIdx.y, L = static_cast<int>(a.L);
+  const int c0 = static_cast<int>(blockIdx.x / ctas) * 64, c = c0 + lane * V, L = static_cast<int>(a.L);
+  const int n = static_cast<int>(blockIdx.z * gridDim.y + blockIdx.y);
+  if (!PACKED && n >= a.N) return;  // all of the cluster
   // with rows that are not aligned C may be odd: the last channel stands alone
   const int width = min(V, a.C - c), there = a.C - c0;
   const bool in = width > 0;
@@ -554,7 +555,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_grad_kernel(const 
   ptx::pdl_wait_prev();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = cluster_rank(), ctas = cluster_size();
-  const int c0 = static_cast<int>(blockIdx.x / ctas) * 64, c = c0 + lane * V, n = blockIdx.y;
+  const int c0 = static_cast<int>(blockIdx.x / ctas) * 64, c = c0 + lane * V;
+  const int n = static_cast<int>(blockIdx.z * gridDim.y + blockIdx.y);
+  if (!PACKED && n >= a.N) return;  // all of the cluster
   const int width = min(V, a.C - c), there = a.C - c0;
   const bool in = width > 0;
   const long long blocks = (a.L + GATED_SCAN_STATE_EVERY - 1) / GATED_SCAN_STATE_EVERY;
@@ -693,13 +696,20 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_grad_kernel(const 
   }
 }
 
-// ddecay: the partial sums [n][C] added in order.
-__global__ void __launch_bounds__(64) gated_scan_sum_kernel(const float* __restrict__ part, float* out, int n, int C) {
+// ddecay: the partial sums [n][C], a thread every 8th of them in order, then the
+// eight in order.
+__global__ void __launch_bounds__(256) gated_scan_sum_kernel(const float* __restrict__ part, float* out, int n, int C) {
+  __shared__ float sums[8][32];
   ptx::pdl_wait_prev();
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  if (c >= C) return;
+  const int c = blockIdx.x * 32 + threadIdx.x;
   float sum = 0.f;
-  for (int k = 0; k < n; ++k) sum += part[static_cast<long long>(k) * C + c];
+  if (c < C)
+    for (int k = threadIdx.y; k < n; k += 8) sum += part[static_cast<long long>(k) * C + c];
+  sums[threadIdx.y][threadIdx.x] = sum;
+  __syncthreads();
+  if (threadIdx.y != 0 || c >= C) return;
+#pragma unroll
+  for (int r = 1; r < 8; ++r) sum += sums[r][threadIdx.x];
   out[c] = sum;
 }
 

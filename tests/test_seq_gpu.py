@@ -676,6 +676,41 @@ def test_bad_offsets_stay_in_bounds(cf):
     assert torch.equal(z[30:], cf.conv_causal(x[30:], w, state=state, cu_seqlens=c - 30)) and (z[:30] == 0).all()
 
 
+def test_many_short_sequences(cf):
+    """Batches past a grid dimension's 65535: as packed, and as their first and last sequences alone."""
+    N, L, C = 70001, 2, 8
+    torch.manual_seed(1)
+    x, r, i, dy = (torch.randn(N, L, C, device="cuda").half() for _ in range(4))
+    decay, w = torch.rand(C, device="cuda"), torch.randn(C, 4, device="cuda").half()
+    ends = torch.tensor([0, 1, 65534, 65535, 65536, N - 1], device="cuda")
+    y, last, states = cf.gated_scan(x, r, i, decay, save_states=True)
+    part = [t[ends] for t in (x, r, i)]
+    ys, ls, ss = cf.gated_scan(*part, decay, save_states=True)
+    assert torch.equal(y[ends], ys) and torch.equal(last[ends], ls)
+    grads, few = cf.gated_scan_grad(x, r, i, decay, dy, states), cf.gated_scan_grad(*part, decay, dy[ends], ss)
+    assert all(torch.equal(a[ends], b) for a, b in zip(grads[:3], few[:3]))
+    cu = (torch.arange(N + 1, device="cuda") * L).int()
+    flat = [t.view(N * L, C) for t in (x, r, i, dy)]
+    yp, lp, sp = cf.gated_scan(*flat[:3], decay, cu_seqlens=cu, save_states=True)
+    assert torch.equal(yp, y.view(N * L, C)) and torch.equal(lp, last)
+    gp = cf.gated_scan_grad(*flat[:3], decay, flat[3], sp, cu_seqlens=cu)
+    assert all(torch.equal(a, b.view(N * L, C)) for a, b in zip(gp[:3], grads[:3]))
+    z, left = cf.conv_causal(x, w, return_state=True)
+    assert torch.equal(z[ends], cf.conv_causal(x[ends], w)) and torch.equal(left[:, 1:], x)
+    assert torch.equal(cf.conv_causal(flat[0], w, cu_seqlens=cu), z.view(N * L, C))
+    dx = cf.conv_causal_grad(x, w, dy)[0]
+    assert torch.equal(dx[ends], cf.conv_causal_grad(x[ends], w, dy[ends])[0])
+    # more runs of a convolution than one grid dimension holds
+    big = (torch.randn(600_000, 1, C, device="cuda") / 16).half()
+    z = cf.conv_causal(big, w)
+    assert torch.equal(z[-5:], cf.conv_causal(big[-5:], w)) and torch.equal(z[530_000:530_005], cf.conv_causal(big[530_000:530_005], w))
+    dx, dw, _, _ = cf.conv_causal_grad(big, w, big)
+    assert torch.equal(dx[-5:], cf.conv_causal_grad(big[-5:], w, big[-5:])[0])
+    ref = (big.double() ** 2).sum((0, 1))
+    # squares: each of 75000 blocks' sums added in eight chains of 9375, and rounded to half: 9383 * 2^-24 + 2^-11
+    assert torch.allclose(dw[:, 3].double(), ref, rtol=1.1e-3)
+
+
 def test_offsets_past_31_bits(cf):
     """More than 2^31 elements: the far end of a long batch is computed as a short one is."""
     C, L = 65536, 33024
