@@ -7,6 +7,11 @@
 // is exact, so that is the only rounding, and a packed block is the same bits
 // wherever it is computed.  A power of two, rather than amax / 127, also makes
 // q * 2^e (7 bits and a sign) exact in the 16-bit types.
+//
+// Bounds: 3.03 bytes an element of a 16-bit type, each way.  Measured, 8 x 4096 x
+// 2560: pack bf16 50 us, 5.1 TB/s (78 % of the copy rate; ALU-bound at 14
+// instructions an element), fp32 63 (6.7 TB/s); unpack bf16 41 us (94 %), fp32 89
+// (73 %: its two 16-byte stores a thread lie 32 bytes apart).
 #pragma once
 
 #include <cstring>
