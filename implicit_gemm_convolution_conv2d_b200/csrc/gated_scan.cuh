@@ -365,8 +365,8 @@ __device__ __forceinline__ Vf<V> scan_exchange(ScanShared<V>& sh, int b, int ord
 
 // The forward pass.  Bounds: 8 bytes an element of a 16-bit type, and five
 // special functions (40 of an SM quarter's cycles for 32 elements, where the
-// bytes take 44).  Measured: 65536 x 2048 bf16 in 364 us, 2.95 TB/s (45 % of the
-// copy rate), 4 x 4096 x 2560 bf16 in 108 us, fp32 in 132 (5.1 TB/s); without
+// bytes take 44).  Measured: 65536 x 2048 bf16 in 360 us, 2.98 TB/s (46 % of the
+// copy rate), 4 x 4096 x 2560 bf16 in 105 us, fp32 in 132 (5.1 TB/s); without
 // its loads or its stores it takes as long, so what bounds it is the issue of
 // some 42 instructions an element at 16 warps an SM and the exchange of a turn.
 // Tokens of a warp: the maps of a turn cost as much however many there are, but
@@ -426,18 +426,24 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const __gri
     }
     Vf<V> av[STEPS], u[STEPS];
     ScanMap<V> mine = no_map<V>();
+    const bool edge = tok.used != kAll || tok.first != 0 || tok.last != 0;
+    const auto gates = [&](auto e) __attribute__((always_inline)) {
+      constexpr bool EDGE = decltype(e)::value;
 #pragma unroll
-    for (int j = 0; j < STEPS; ++j) {
-      const GateValues<V> g = gate_values<V>(a.consts, gate_input<T, V>(row_pair(tile.r, j, lane)),
-                                             gate_input<T, V>(row_pair(tile.i, j, lane)), decay);
-      Vf<V> xv;
-      unpack<T, V>(row_pair(tile.x, j, lane), xv.v);
-      u[j] = gated_input<V>(g, g.m, xv);
-      av[j] = g.a;
-      if (PACKED && (tok.first >> j & 1))
-        mine = ScanMap<V>{splat<V>(-1.f), scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, width)};
-      then_token<PACKED>(mine, av[j], u[j]);
-    }
+      for (int j = 0; j < STEPS; ++j) {
+        const GateValues<V> g = gate_values<V>(a.consts, gate_input<T, V>(row_pair(tile.r, j, lane)),
+                                               gate_input<T, V>(row_pair(tile.i, j, lane)), decay);
+        Vf<V> xv;
+        unpack<T, V>(row_pair(tile.x, j, lane), xv.v);
+        u[j] = gated_input<V>(g, g.m, xv);
+        av[j] = g.a;
+        if (EDGE && (tok.first >> j & 1))
+          mine = ScanMap<V>{splat<V>(-1.f), scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, width)};
+        then_token<EDGE>(mine, av[j], u[j]);
+      }
+    };
+    if (PACKED && edge) gates(std::true_type{});
+    else gates(std::false_type{});
     __syncwarp();
     const auto load = [&] {
       r.next(span);
@@ -454,19 +460,24 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const __gri
       put_state<V>(a.states,
                    n * ((a.L + GATED_SCAN_STATE_EVERY - 1) / GATED_SCAN_STATE_EVERY) + (L - left) / GATED_SCAN_STATE_EVERY,
                    a.C, c, width, h);
-    T* out = y;
+    const auto apply = [&](auto e) __attribute__((always_inline)) {
+      constexpr bool EDGE = decltype(e)::value;
+      T* out = y;
 #pragma unroll
-    for (int j = 0; j < STEPS; ++j, out += a.C) {
-      if (PACKED && (tok.first >> j & 1))
-        h = scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, width);
-      h = fma_v(av[j], h, u[j]);
-      if (in && (tok.used >> j & 1)) put_row<T, V, ALIGNED>(out, width, h);
-      else if (PACKED && in && a.fill && j < left) put_row<T, V, ALIGNED>(out, width, splat<V>(0.f));
-      if (PACKED && (tok.last >> j & 1)) {
-        const int s = __shfl_sync(0xffffffffu, tok.seq, j);
-        if (in && a.h_last) put_state<V>(a.h_last, s, a.C, c, width, h);
+      for (int j = 0; j < STEPS; ++j, out += a.C) {
+        if (EDGE && PACKED && (tok.first >> j & 1))
+          h = scan_initial<V>(a.h0, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, width);
+        h = fma_v(av[j], h, u[j]);
+        if (in && (!EDGE || (tok.used >> j & 1))) put_row<T, V, ALIGNED>(out, width, h);
+        else if (EDGE && PACKED && in && a.fill && j < left) put_row<T, V, ALIGNED>(out, width, splat<V>(0.f));
+        if (EDGE && PACKED && (tok.last >> j & 1)) {
+          const int s = __shfl_sync(0xffffffffu, tok.seq, j);
+          if (in && a.h_last) put_state<V>(a.h_last, s, a.C, c, width, h);
+        }
       }
-    }
+    };
+    if (edge) apply(std::true_type{});
+    else apply(std::false_type{});
     if constexpr (!ALIGNED) load();
   }
   copies_done();
