@@ -14,10 +14,10 @@
 // multiplied by zero, as x may be infinite there.
 //
 // Bounds: 4 bytes an element of a 16-bit type, 6 for the gradients.  Measured,
-// K = 4 with silu: 8 x 4096 x 2560 bf16 in 73 us, 4.6 TB/s (70 % of the copy
-// rate), fp32 in 119 (5.65 TB/s); a thread of 8 channels that loaded straight
-// into registers took 124.  Its gradients: 152 us, 3.3 TB/s (51 %), from
-// checkpoints 178; they issue some 30 instructions an element at 54 % of the
+// K = 4 with silu: 8 x 4096 x 2560 bf16 in 67 us, 5.0 TB/s (77 % of the copy
+// rate), fp32 in 121 (5.5 TB/s); a thread of 8 channels that loaded straight
+// into registers took 124.  Its gradients: 138 us, 3.65 TB/s (56 %), from
+// checkpoints 160; they issue some 30 instructions an element at 54 % of the
 // rate, each waiting 2.4 cycles for the one in front of it at 16 warps an SM.
 #pragma once
 

@@ -103,7 +103,7 @@ def unpack_args(**k):
 REFUSED = [
     ("conv_causal", conv_args, [
         (dict(dtype=9), EDTYPE), (dict(K=0), EINVAL), (dict(K=9), EINVAL), (dict(C=0), EINVAL), (dict(N=-1), EINVAL),
-        (dict(L=-1), EINVAL), (dict(L=1 << 31), EINVAL), (dict(act=2), EINVAL), (dict(x=None), EINVAL), (dict(w=None), EINVAL),
+        (dict(L=-1), EINVAL), (dict(L=1 << 31), EINVAL), (dict(L=(1 << 31) - 4096), EINVAL), (dict(act=2), EINVAL), (dict(x=None), EINVAL), (dict(w=None), EINVAL),
         (dict(y=None), EINVAL), (dict(xt=-1), EINVAL), (dict(xb=-1), EINVAL), (dict(xt=1 << 60), EINVAL), (dict(x=at(0) + 1), EALIGN),
         (dict(y=at(4) + 1), EALIGN), (dict(cu=at(6) + 2), EALIGN), (dict(y=at(0) + 64), EALIAS), (dict(state_out=at(3)), EALIAS),
         (dict(y=at(1)), EALIAS), (dict(state_out=at(4) + 32), EALIAS)]),
