@@ -245,10 +245,12 @@ def conv_wgrad(x, dy, kernel_size, stride=1, padding=0, dilation=1, groups=1, *,
     if isinstance(x, Act8):
         if not (x.q.is_cuda and dy.is_cuda):
             raise ValueError("conv_wgrad runs on CUDA tensors only")
-        st = stream if stream is not None else torch.cuda.current_stream(dy.device)
-        with torch.cuda.stream(st):
-            return conv_wgrad(act8_unpack(x), dy, kernel_size, stride, padding, dilation, groups,
-                              padding_hi=padding_hi, out=out, workspace=workspace)
+        if stream is not None:  # the temporary belongs to the stream that it is used on
+            with torch.cuda.stream(stream):
+                return conv_wgrad(x, dy, kernel_size, stride, padding, dilation, groups, padding_hi=padding_hi, out=out,
+                                  workspace=workspace)
+        return conv_wgrad(act8_unpack(x), dy, kernel_size, stride, padding, dilation, groups, padding_hi=padding_hi,
+                          out=out, workspace=workspace)
     if not (x.is_cuda and dy.is_cuda):
         raise ValueError("conv_wgrad runs on CUDA tensors only")
     if x.dtype != dy.dtype:
