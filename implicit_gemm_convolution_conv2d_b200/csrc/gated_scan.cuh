@@ -27,12 +27,12 @@ namespace convfwd {
 // so that they are operands of an instruction (an immediate pair is not: it
 // costs two moves each time).
 struct GateConsts {
-  float2 nlog2e, one, nhalf, p3, p4, p5, p6, two, none;
+  float2 nlog2e, one, nhalf, p3, p4, p5, p6, two, none, unit;
 };
 inline GateConsts gate_consts() {
   const auto two = [](float v) { return make_float2(v, v); };
   return GateConsts{two(-kLog2e),        two(1.f),           two(-0.5f), two(1.f / 6.f), two(-1.f / 24.f),
-                    two(1.f / 120.f), two(-1.f / 720.f), two(2.f),   two(-1.f)};
+                    two(1.f / 120.f), two(-1.f / 720.f), two(2.f),   two(-1.f),      two(0x1p-124f)};
 }
 template <int V>
 __device__ __forceinline__ Vf<V> both(const float2& c) {
@@ -42,29 +42,43 @@ __device__ __forceinline__ Vf<V> both(const float2& c) {
   return o;
 }
 
-// The sigmoids share a reciprocal, 1 / ((1 + e^-r)(1 + e^-i)): the special
-// functions, 16 a clock and SM, are the first limit of these kernels, and this
-// leaves 5 of them an element.  So that the product stays finite r and i stop
-// at -44, and e^-44 (a little more, for the reciprocal's error) is taken off
-// the sigmoids again: a gate is exactly 0 there, at -infinity too, and off by
-// less than 2^-63 in front of it.  The subtraction saturates to [0, 1], which
-// makes a NaN 0, so u takes the reciprocal times 0 with it.
-constexpr float kGateLowest = -44.f;
-constexpr float kGateFloor = 7.79e-20f;  // e^-44 = 7.781e-20
+// The sigmoids of the forward pass share a reciprocal: the special functions, 16 a
+// clock and SM, are its first limit, and this leaves 5 of them an element (with 6,
+// 65536 x 2048 bf16 takes 381 us in place of 367).  With E_r = 1 + e^-r and E_i =
+// 2^-124 (1 + e^-i) the product E_r E_i is a normal number unless both gates are
+// below 2^-124 (where both then are 0), so s = E_i / (E_r E_i) and g = 2^-124 E_r /
+// (E_r E_i) are right down to fp32's least normal number, at r or i = -87.3.
+// Below, at -infinity too, they are 0: r and i stop at -87.5, and the last product
+// takes what is subnormal as 0.  A NaN in either gate makes both NaN, as it makes
+// u = m g x and every state behind it.
+//
+// In the backward pass that would be wrong, as a NaN in i leaves a, and through it
+// the gradients of earlier tokens, as they are: there each sigmoid has a reciprocal
+// of its own, whose flush of subnormal results closes the gates at the same place.
+constexpr float kGateLowest = -87.5f;  // exact in each type; e^87.5 is finite
 
-__device__ __forceinline__ float fma_sat(float a, float b, float c) {
-  float y;
-  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
+// a b, with subnormal results as 0
+template <int V>
+__device__ __forceinline__ Vf<V> mul_ftz(const Vf<V>& a, const Vf<V>& b) {
+  Vf<V> o;
+#pragma unroll
+  for (int k = 0; k + 1 < V; k += 2) {
+    uint64_t d;
+    asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pack2(a.v + k)), "l"(pack2(b.v + k)));
+    unpack2(d, o.v + k);
+  }
+  if constexpr (V & 1) asm("mul.rn.ftz.f32 %0, %1, %2;" : "=f"(o[V - 1]) : "f"(a[V - 1]), "f"(b[V - 1]));
+  return o;
 }
 
 template <int V>
 struct GateValues {
-  Vf<V> s, g, a, m, nan;  // nan: 0, or NaN where r or i is
+  Vf<V> s, g, a, m;
 };
 
-// r and i at least kGateLowest.  IN_ROOT: m = sqrt(1 - a^2); else 1 - a^2.
-template <int V, bool IN_ROOT = true>
+// FORWARD: a shared reciprocal, r and i at least kGateLowest, and m = sqrt(1 - a^2);
+// else a reciprocal each, any r and i, and 1 - a^2 in m.
+template <int V, bool FORWARD = true>
 __device__ __forceinline__ GateValues<V> gate_values(const GateConsts& c, const Vf<V>& r, const Vf<V>& i,
                                                      const Vf<V>& decay) {
   GateValues<V> o;
@@ -73,15 +87,19 @@ __device__ __forceinline__ GateValues<V> gate_values(const GateConsts& c, const 
 #pragma unroll
   for (int k = 0; k < V; ++k) er[k] = ex2_approx(er[k]), ei[k] = ex2_approx(ei[k]);
   er = add_v(er, one);
-  ei = add_v(ei, one);
-  Vf<V> inv = mul_v(er, ei);
+  if constexpr (FORWARD) {
+    const Vf<V> unit = both<V>(c.unit);
+    ei = fma_v(ei, unit, unit);
+    Vf<V> inv = mul_v(er, ei);
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    inv[k] = rcp_approx(inv[k]);
-    o.s[k] = fma_sat(inv[k], ei[k], -kGateFloor);
-    o.g[k] = fma_sat(inv[k], er[k], -kGateFloor);
+    for (int k = 0; k < V; ++k) inv[k] = rcp_approx(inv[k]);
+    o.s = mul_ftz(inv, ei);
+    o.g = mul_ftz(mul_v(inv, er), unit);
+  } else {
+    ei = add_v(ei, one);
+#pragma unroll
+    for (int k = 0; k < V; ++k) o.s[k] = rcp_approx(er[k]), o.g[k] = rcp_approx(ei[k]);
   }
-  o.nan = inv;
   const Vf<V> w = mul_v(decay, o.s);  // -l
   // 1 - e^-w = w (1 - w/2 + w^2/6 - w^3/24 + w^4/120 - w^5/720); the next term
   // is w^6/5040 < 5e-8 of it for w < 1/4
@@ -101,16 +119,15 @@ __device__ __forceinline__ GateValues<V> gate_values(const GateConsts& c, const 
     o.a[k] = near1 ? near_a[k] : far[k];
   }
   o.m = mul_v(E, fma_v(E, none, both<V>(c.two)));
-  if constexpr (IN_ROOT) {
+  if constexpr (FORWARD) {
 #pragma unroll
     for (int k = 0; k < V; ++k) o.m[k] = sqrt_approx(o.m[k]);
   }
   return o;
 }
-// m g x, and NaN where a gate is
 template <int V>
 __device__ __forceinline__ Vf<V> gated_input(const GateValues<V>& v, const Vf<V>& m, const Vf<V>& x) {
-  return fma_v(v.nan, splat<V>(0.f), mul_v(mul_v(m, v.g), x));
+  return mul_v(mul_v(m, v.g), x);
 }
 
 template <int V>
@@ -635,13 +652,11 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_grad_kernel(const 
     ScanMap<V> fwd = no_map<V>(), bwd = no_map<V>();
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
-      const GateValues<V> gv = gate_values<V, false>(a.consts, gate_input<T, V>(row_pair(tile.r, j, lane)),
-                                                     gate_input<T, V>(row_pair(tile.i, j, lane)), decay);
+      const GateValues<V> gv = gate_values<V, false>(a.consts, row_of(tile.r, j), row_of(tile.i, j), decay);
 #pragma unroll
       for (int k = 0; k < V; ++k) over[j][k] = gv.m[k] > 0.f ? rsqrt_approx(gv.m[k]) : gv.m[k];
       mv[j] = mul_v(gv.m, over[j]);
-      const Vf<V> sv = fma_v(gv.nan, splat<V>(0.f), gv.s);  // NaN where a gate is
-      sh.s[warp][j][lane] = make_float2(sv[0], sv[1]);
+      sh.s[warp][j][lane] = make_float2(gv.s[0], gv.s[1]);
       g[j] = gv.g;
       av[j] = gv.a;
       if (PACKED && (tok.first >> j & 1))
@@ -682,6 +697,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_grad_kernel(const 
     for (int j = STEPS - 1; j >= 0; --j) {
       if (PACKED && (tok.last >> j & 1))
         G = scan_initial<V>(a.dh_last, __shfl_sync(0xffffffffu, tok.seq, j), a.C, c, width);
+      // a token's reads stay behind the one's in front: read ahead they spill 100 bytes
+      // (16000 x 2048 f16 packed, from checkpoints: 282 us with them, 248 without)
+      if (PACKED) __syncwarp();
       const Vf<V> one = both<V>(a.consts.one), none1 = both<V>(a.consts.none);
       const Vf<V> whole = add_v(row_of(tile.dy, j), G), vx = mul_v(g[j], row_of(tile.x, j));
       const Vf<V> Gm = mul_v(whole, pair_of(tile.m[j][lane]));
