@@ -71,6 +71,10 @@ __device__ __forceinline__ Vf<V> mul_ftz(const Vf<V>& a, const Vf<V>& b) {
   return o;
 }
 
+// Where 1 - a^2 is less (decay s under 6e-39), the approximate roots take it as 0: m
+// is 0 in the forward pass, and in the backward pass, whose 1 / m would be infinite.
+constexpr float kLeastNormal = 0x1p-126f;
+
 template <int V>
 struct GateValues {
   Vf<V> s, g, a, m;
@@ -647,14 +651,15 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_grad_kernel(const 
       unpack<T, V>(row_pair(t, j, lane), v.v);
       return v;
     };
-    Vf<V> av[STEPS], g[STEPS], over[STEPS];  // over: 1 / m, 0 where a = 1; s and m go to shared memory
+    // over: 1 / m, next to 0 where a = 1; s and m go to shared memory
+    Vf<V> av[STEPS], g[STEPS], over[STEPS];
     Vf<V> mv[STEPS];
     ScanMap<V> fwd = no_map<V>(), bwd = no_map<V>();
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
       const GateValues<V> gv = gate_values<V, false>(a.consts, row_of(tile.r, j), row_of(tile.i, j), decay);
 #pragma unroll
-      for (int k = 0; k < V; ++k) over[j][k] = gv.m[k] > 0.f ? rsqrt_approx(gv.m[k]) : gv.m[k];
+      for (int k = 0; k < V; ++k) over[j][k] = gv.m[k] >= kLeastNormal ? rsqrt_approx(gv.m[k]) : gv.m[k];
       mv[j] = mul_v(gv.m, over[j]);
       sh.s[warp][j][lane] = make_float2(gv.s[0], gv.s[1]);
       g[j] = gv.g;

@@ -104,8 +104,9 @@ int gated_scan(const void* x, const void* r, const void* i, const float* decay, 
  * all tensors, or all contiguous checkpoints; CONV_EUNSUPPORTED where they are
  * mixed or strided) and its `states`: dx, dr, di (like y), ddecay
  * [C] and dh0 [N, C] (fp32; dh0 may be NULL).  dh_last (fp32, may be NULL) is
- * the gradient of h_last.  With a = 1 (decay * s = 0) the square root's
- * derivative is taken as 0.  ddecay is summed as dw above is. */
+ * the gradient of h_last.  Where 1 - a^2 is below fp32's least normal number
+ * (decay * s under 6e-39, or 0) it counts as 0, as in the forward pass, and the
+ * square root's derivative is taken as 0.  ddecay is summed as dw above is. */
 int gated_scan_grad(const void* x, const unsigned char* x_scale, const void* r, const unsigned char* r_scale,
                     const void* i, const unsigned char* i_scale, const float* decay, const float* states,
                     const float* h0, const int* cu, const void* dy, const float* dh_last, void* dx, void* dr, void* di,

@@ -1,5 +1,5 @@
-"""The gated recurrence where its gates are at their ends, on the GPU: closed gates and gates that are NaN, against the
-64-bit forms."""
+"""The gated recurrence where its gates are at their ends, on the GPU: closed gates, gates that are NaN and decays next
+to 0, against the 64-bit forms."""
 from __future__ import annotations
 
 import pytest
@@ -131,3 +131,33 @@ def test_gradients_beside_a_nan_gate(cf, dtype, which, cu, saved8):
     for k, t in gg.items():
         # the states that the backward pass starts from are the kernel's own: off by no more than y's bound, as in the bounds
         ok(t, grads[k], bound["d" + k], torch.float32 if k in ("decay", "h0") else dt, "d" + k)
+
+
+# ---- decays at their ends -----------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_least_decays(cf, dtype):
+    """Where 1 - a^2 is no normal number of fp32 it counts as 0, in both passes; beside that, the definition."""
+    g, dt, L = gen(62), DT[dtype], 140
+    decay = torch.tensor([0.0, 1e-45, 1e-42, 1e-39, 6e-39, 1.2e-38, 2e-38, 1e-37, 1e-30, 1e-20, 1e-9, 1e-3])
+    C = len(decay)
+    x, r, i, dy = (normal(g, 2, L, C, dtype=dt) for _ in range(4))
+    r[0, 5::9, 8:10] = -40.0  # 1 - a^2 = 8e-48 and 8e-38
+    h0, dh_last = normal(g, 2, C), normal(g, 2, C)
+    y, last, grads, bound = reference(x, r, i, decay.clamp(min=1e-45), h0, None, dy, dh_last)
+    gy, gl, gg = both_passes(cf, x, r, i, decay, h0, None, dy, dh_last)
+    # what 1 - a^2 below the least number would have given: m < 2^-63, of each token
+    rest = L * 2.0 ** -63 * x.double().abs().max()
+    ok(gy, y, bound["y"] + rest, dt, "y")
+    ok(gl, last, bound["last"] + rest, torch.float32, "h_last")
+    for t in gg.values():
+        assert torch.isfinite(t).all()
+    most = (dy.double().abs().max() * L + dh_last.double().abs().max())  # of |G|
+    ok(gg["x"], grads["x"], bound["dx"] + most * 2.0 ** -63, dt, "dx")
+    ok(gg["i"], grads["i"], bound["di"] + most * rest, dt, "di")
+    # decay s |G| a g |x| / m <= m |G x|, as 1 - a^2 <= 2 decay s
+    ok(gg["r"], grads["r"], bound["dr"] + 2 * most * rest, dt, "dr")
+    ok(gg["h0"], grads["h0"], bound["dh0"], torch.float32, "dh0")
+    ok(gg["decay"][10:], grads["decay"][10:], bound["ddecay"][10:], torch.float32, "ddecay")
+    assert (gg["x"][..., :2] == 0).all()
