@@ -279,6 +279,16 @@ __device__ __forceinline__ Vf<V> scan_initial(const float* h0, long long s, int 
   for (int k = 0; k < V; ++k) h[k] = h0 && k < width ? __ldg(h0 + s * C + c + k) : 0.f;
   return h;
 }
+// The decays of channels c .. c + width - 1.  An infinite one counts as the largest
+// number: a is 0 all the same, and infinity times a closed gate, of which tokens
+// that are not there are made, would be NaN.
+template <int V>
+__device__ __forceinline__ Vf<V> load_decay(const float* decay, int c, int width) {
+  Vf<V> d = scan_initial<V>(decay, 0, 0, c, width);
+#pragma unroll
+  for (int k = 0; k < V; ++k) d[k] = min_nan(d[k], 0x1.fffffep127f);
+  return d;
+}
 template <int V>
 __device__ __forceinline__ void put_state(float* h, long long s, int C, int c, int width, const Vf<V>& v) {
 #pragma unroll
@@ -421,7 +431,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const __gri
   const int width = min(V, a.C - c), there = a.C - c0;
   const bool in = width > 0;
   auto& tile = sh.warp[warp];
-  const Vf<V> decay = scan_initial<V>(a.decay, 0, a.C, c, width);
+  const Vf<V> decay = load_decay<V>(a.decay, c, width);
   Vf<V> carry = PACKED ? splat<V>(0.f) : scan_initial<V>(a.h0, n, a.C, c, width);
   if (PACKED) pass_empty<V>(a, a.h0, a.h_last, rank * kScanWarps + warp, ctas * kScanWarps, c, width);
   if (ctas > 1) cluster_arrive(false), cluster_wait();  // every CTA runs before another writes to its shared memory
@@ -610,7 +620,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_grad_kernel(const 
   const int width = min(V, a.C - c), there = a.C - c0;
   const bool in = width > 0;
   const long long blocks = (a.L + GATED_SCAN_STATE_EVERY - 1) / GATED_SCAN_STATE_EVERY;
-  const Vf<V> decay = scan_initial<V>(a.decay, 0, a.C, c, width);
+  const Vf<V> decay = load_decay<V>(a.decay, c, width);
   Vf<V> carry = PACKED ? splat<V>(0.f) : scan_initial<V>(a.dh_last, n, a.C, c, width), dd = splat<V>(0.f);
   if (PACKED) pass_empty<V>(a, a.dh_last, a.dh0, rank * kScanWarps + warp, ctas * kScanWarps, c, width);
   if (ctas > 1) cluster_arrive(false), cluster_wait();  // every CTA runs before another writes to its shared memory
@@ -792,10 +802,11 @@ __global__ void __launch_bounds__(kStepThreads) gated_scan_step_kernel(const Sca
     if (a.fill) store_zero<T, V>(y + static_cast<long long>(b) * a.C);
     return;
   }
-  Vf<V> decay, h;
+  const Vf<V> decay = load_decay<V>(a.decay, c, V);
+  Vf<V> h;
   float* hp = a.h + static_cast<long long>(slot) * a.C + c;
 #pragma unroll
-  for (int k = 0; k < V; ++k) decay[k] = __ldg(a.decay + c + k), h[k] = hp[k];
+  for (int k = 0; k < V; ++k) h[k] = hp[k];
   do {
     Vf<V> x, r, i;
     unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.x) + b * a.xs + c), x.v);

@@ -85,8 +85,8 @@ int conv_causal_step(const void* x, const void* w, const void* bias, void* state
  *   h[t] = a * h[t-1] + sqrt(1 - a^2) * g * x[t],   y[t] = h[t]
  *
  * for each channel within each sequence, from h0 [N, C] (fp32; zero if NULL).
- * decay: [C] fp32, >= 0.  A sigmoid below fp32's least normal number (a gate
- * under -87.3) is 0.  The state and all sums are fp32; y is h rounded to
+ * decay: [C] fp32, >= 0; an infinite one counts as fp32's largest number.  A
+ * sigmoid below fp32's least normal number (a gate under -87.3) is 0.  The state and all sums are fp32; y is h rounded to
  * the type of x, r and i.  h_last [N, C] (fp32, may be NULL) receives each
  * sequence's last state (h0 for an empty one).  states (fp32, may be NULL)
  * receives the state in front of every GATED_SCAN_STATE_EVERY-th token,

@@ -1,5 +1,5 @@
-"""The gated recurrence where its gates are at their ends, on the GPU: closed gates, gates that are NaN and decays next
-to 0, against the 64-bit forms."""
+"""The gated recurrence where its gates are at their ends, on the GPU: closed gates, gates that are NaN, decays next to
+0 and infinite ones, against the 64-bit forms."""
 from __future__ import annotations
 
 import pytest
@@ -161,3 +161,29 @@ def test_least_decays(cf, dtype):
     ok(gg["h0"], grads["h0"], bound["dh0"], torch.float32, "dh0")
     ok(gg["decay"][10:], grads["decay"][10:], bound["ddecay"][10:], torch.float32, "ddecay")
     assert (gg["x"][..., :2] == 0).all()
+
+
+@pytest.mark.parametrize("L", [1, 64, 100, 128, 333])
+@pytest.mark.parametrize("dtype", DT)
+def test_infinite_decay_keeps_nothing(cf, dtype, L):
+    """a = 0: y = sigmoid(i) x, and each token's gradients are its own; at any length, the state that is left too."""
+    g, dt, C = gen(63), DT[dtype], 40
+    x, r, i, dy = (normal(g, 2, L, C, dtype=dt) for _ in range(4))
+    decay, h0, dh_last = torch.full((C,), float("inf")), normal(g, 2, C), normal(g, 2, C)
+    decay[1::3] = torch.finfo(torch.float32).max
+    big = torch.full((C,), 1e30)  # a = 0 in 64 bits too
+    y, last, grads, bound = reference(x, r, i, big, h0, None, dy, dh_last)
+    gy, gl, gg = both_passes(cf, x, r, i, decay, h0, None, dy, dh_last)
+    units = lambda v: R.U * (R.sigmoid_units(v.double()) + 4)  # noqa: E731
+    ok(gy, y, y.abs() * units(i), dt, "y")
+    ok(gl, last, last.abs() * units(i[:, -1]), torch.float32, "h_last")
+    ok(gg["x"], grads["x"], grads["x"].abs() * units(i), dt, "dx")
+    s = torch.sigmoid(i.double())
+    G = dy.double().clone()
+    G[:, -1] += dh_last
+    ok(gg["i"], grads["i"], R.U * (G * x.double() * s).abs() * ((R.sigmoid_units(i.double()) + 6) * (1 + s)), dt, "di")
+    for k in ("r", "decay", "h0"):
+        assert (gg[k] == 0).all() and (grads[k] == 0).all(), k
+    pool = h0.cuda()
+    z = cf.gated_scan_step(x[:, 0].cuda(), r[:, 0].cuda(), i[:, 0].cuda(), decay.cuda(), pool)
+    ok(z, y[:, 0], (y.abs() * units(i))[:, 0], dt, "step")
