@@ -118,6 +118,12 @@ def _same_device(like, what, names, *tensors):
             raise ValueError(f"{what}: {name} is on {t.device}, x on {like.device}")
 
 
+def _fits(what, *sizes):
+    """The library takes these as 32-bit integers, and ctypes would cut them off."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"{what}: sequences, rows of a step, slots and channels are at most 2^31 - 1, not {max(sizes)}")
+
+
 def _extents(x, cu, what):
     """(N, L, C) of tokens: [N, L, C], or packed [L, C] with N sequences."""
     if cu is None:
@@ -135,6 +141,7 @@ def _extents(x, cu, what):
         N = cu.shape[0] - 1
     if C < 1:
         raise ValueError(f"{what}: x has no channels")
+    _fits(what, N, C)
     return N, L, C
 
 
@@ -210,6 +217,7 @@ def act8_pack(x, *, stream=None) -> Act8:
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError(f"{what}: x must be [..., C]")
     C = x.shape[-1]
+    _fits(what, C)
     there = _elsewhere(x, stream)
     if there is not None:
         with there:
@@ -232,7 +240,10 @@ def act8_unpack(p: Act8, *, out=None, stream=None):
         raise TypeError(f"{what}: takes an Act8")
     q, scale, dtype = _saved(p, what, "p")
     code = _code(dtype, what)
+    if q.dim() < 1 or q.shape[-1] < 1:
+        raise ValueError(f"{what}: p must be [..., C]")
     C = q.shape[-1]
+    _fits(what, C)
     _same_device(q, what, "out", out)
     there = _elsewhere(q, stream)
     if there is not None:
@@ -341,6 +352,7 @@ def _step_rows(x, pool_rows, index, what):
     if x.dim() != 2 or x.shape[1] < 1:
         raise ValueError(f"{what}: x must be [B, C]")
     B = x.shape[0]
+    _fits(what, B, pool_rows, x.shape[1])
     if index is None:
         if B > pool_rows:
             raise ValueError(f"{what}: {B} rows but {pool_rows} slots: give an index")
