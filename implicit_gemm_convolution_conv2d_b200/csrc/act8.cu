@@ -52,7 +52,7 @@ extern "C" {
 int act8_pack(const void* x, signed char* q, unsigned char* scale, long long rows, int C, long long x_row, int dtype,
               conv_stream_t stream) {
   if (!dtype_ok(dtype)) return CONV_EDTYPE;
-  if (rows < 0 || C <= 0 || rows > kSeqMaxElems / C) return CONV_EINVAL;
+  if (rows < 0 || C <= 0 || C > kSeqMaxCount || rows > kSeqMaxElems / C) return CONV_EINVAL;
   long long xe;
   if (x_row < 0 || x_row > kSeqMaxElems || (rows > 1 && x_row > kSeqMaxElems / (rows - 1))) return CONV_EINVAL;
   if (rows == 0) return CONV_OK;
@@ -72,7 +72,7 @@ int act8_pack(const void* x, signed char* q, unsigned char* scale, long long row
 int act8_unpack(const signed char* q, const unsigned char* scale, void* y, long long rows, int C, int dtype,
                 conv_stream_t stream) {
   if (!dtype_ok(dtype)) return CONV_EDTYPE;
-  if (rows < 0 || C <= 0 || rows > kSeqMaxElems / C) return CONV_EINVAL;
+  if (rows < 0 || C <= 0 || C > kSeqMaxCount || rows > kSeqMaxElems / C) return CONV_EINVAL;
   if (rows == 0) return CONV_OK;
   if (!q || !scale || !y) return CONV_EINVAL;
   const int es = elem_size(dtype);

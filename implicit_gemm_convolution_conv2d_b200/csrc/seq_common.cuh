@@ -253,11 +253,13 @@ constexpr long long kSeqMaxElems = 1LL << 46;  // of a tensor, and of a stride: 
 inline int elem_size(int dtype) { return dtype == CONV_F32 ? 4 : 2; }
 inline bool dtype_ok(int dtype) { return dtype == CONV_F32 || dtype == CONV_F16 || dtype == CONV_BF16; }
 
-constexpr long long kSeqMaxTokens = 0x7fffffffLL - 4096;  // of a sequence: places behind its end fit 32 bits too
+// Tokens of a sequence, sequences and channels: places behind the last (a warp's
+// share, a block of 32 channels) fit 32 bits too.
+constexpr long long kSeqMaxCount = 0x7fffffffLL - 4096;
 
 // N sequences of L rows of C channels (packed: L rows in all): sizes that fit.
 inline bool seq_sizes_ok(int N, long long L, long long C, bool packed) {
-  if (N < 0 || L < 0 || C <= 0 || L > kSeqMaxTokens) return false;
+  if (N < 0 || L < 0 || C <= 0 || N > kSeqMaxCount || L > kSeqMaxCount || C > kSeqMaxCount) return false;
   const long long rows = packed ? L : L * N;  // both below 2^31
   return rows <= kSeqMaxElems / C && N <= kSeqMaxElems / C;
 }

@@ -14,8 +14,8 @@
  *    their output rows are left as they are, or with fill = 1 set to zero.
  *    cu is read on the device and not checked; entries that decrease or lie
  *    outside [0, L] give unspecified results but no access out of bounds.
- * N, L and the step functions' B may be 0; L is at most 2^31 - 4097.  C is any
- * positive number.  A workspace is in use until the call's kernels are done:
+ * N, L and the step functions' B may be 0; C is at least 1; none is above
+ * 2^31 - 4097.  A workspace is in use until the call's kernels are done:
  * calls that may overlap (other streams, graphs replayed side by side) need one
  * each.
  * Inputs documented with strides have unit channel stride, a token stride and

@@ -43,3 +43,46 @@ def test_sizes_past_32_bits_are_refused(seq):
         with pytest.raises(ValueError, match=r"2\^31"):
             call()
             pytest.fail(f"call {k} was not refused")
+
+
+# ---- the library --------------------------------------------------------
+
+
+@pytest.fixture(scope="module")
+def T():
+    import tests.test_seq_cpu as T
+    return T
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from implicit_gemm_convolution_conv2d_b200 import _build, seq
+    _build.build()
+    return seq._lib()
+
+
+TOP = 2 ** 31 - 4096  # the first number that is refused
+
+
+def test_last_channels_and_sequences_are_refused(lib, T):
+    """Places behind the last channel or sequence fit 32 bits; C and N that they would not fit are refused (one row, one
+    token or none, so that nothing else is too large)."""
+    for C in (TOP, 2 ** 31 - 1):
+        one = dict(N=1, L=1, C=C, cu=None)
+        step = dict(B=1, slots=1, C=C, index=None)
+        assert lib["conv_causal"](*T.conv_args(**one, K=1, state=None, state_out=None, y=1 << 40, w=1 << 50, bias=None)) == T.EINVAL
+        assert lib["conv_causal_grad"](*T.conv_grad_args(**one, K=1, state=None, ds=None, dso=None, bias=None, db=None, w=1 << 50, dy=1 << 51,
+                                                         dx=1 << 52, dw=1 << 53, ws=1 << 54, wb=1 << 40)) == T.EINVAL
+        assert lib["conv_causal_step"](*T.conv_step_args(**step, K=1, bias=None, w=1 << 50, y=1 << 51)) == T.EINVAL
+        assert lib["gated_scan"](*T.scan_args(**one, x=1 << 50, r=1 << 51, i=1 << 52, decay=1 << 53, h0=None, y=1 << 54, last=None,
+                                              states=None)) == T.EINVAL
+        assert lib["gated_scan_step"](*T.scan_step_args(**step, x=1 << 50, r=1 << 51, i=1 << 52, decay=1 << 53, h=1 << 54, y=1 << 55)) == T.EINVAL
+        assert lib["act8_pack"](*T.pack_args(rows=1, C=C, q=1 << 50, scale=1 << 51)) == T.EINVAL
+        assert lib["act8_unpack"](*T.unpack_args(rows=1, C=C, scale=1 << 50, y=1 << 51)) == T.EINVAL
+        n = T.ctypes.c_ulonglong()
+        assert lib["conv_causal_grad_workspace_size"](1, 1, C, 1, 0, T.ctypes.byref(n)) == T.EINVAL
+        assert lib["gated_scan_grad_workspace_size"](1, 1, C, 0, T.ctypes.byref(n)) == T.EINVAL
+    for N in (TOP, 2 ** 31 - 1):
+        for L, cu in ((0, None), (5, 1 << 55)):
+            assert lib["conv_causal"](*T.conv_args(N=N, L=L, C=1, K=1, cu=cu, xb=0, xt=1, state=None, state_out=None, bias=None)) == T.EINVAL
+            assert lib["gated_scan"](*T.scan_args(N=N, L=L, C=1, cu=cu, xb=0, rb=0, ib=0, h0=None, last=1 << 50, states=None)) == T.EINVAL
