@@ -474,8 +474,8 @@ __global__ void __launch_bounds__(128) conv_causal_dstate_kernel(const __grid_co
   ptx::pdl_wait_prev();
   const int c = blockIdx.x * 128 + threadIdx.x, K = a.K;
   if (c >= a.C) return;
-  for (int s = blockIdx.y; s < a.N; s += gridDim.y) {
-    const int n = a.cu ? 0 : s;
+  for (long long next = blockIdx.y; next < a.N; next += gridDim.y) {  // may pass 31 bits behind the last
+    const int s = static_cast<int>(next), n = a.cu ? 0 : s;
     SeqAt q{s, 0, a.L};
     if (a.cu) {
       q.begin = max(0, min(a.L, __ldg(a.cu + s)));

@@ -187,7 +187,7 @@ __device__ __forceinline__ float act8_step(unsigned char s) {
 __device__ __forceinline__ int seq_of_row(const int* __restrict__ cu, int n, long long t) {
   int lo = 0, hi = n;  // the number of ends cu[1..n] that are <= t
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
+    const int mid = lo + ((hi - lo) >> 1);  // the sum may pass 31 bits
     if (__ldg(cu + mid + 1) <= t) lo = mid + 1; else hi = mid;
   }
   if (lo < n && t < __ldg(cu + lo)) lo = n;  // in front of the first sequence
