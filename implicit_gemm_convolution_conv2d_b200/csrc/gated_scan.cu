@@ -91,8 +91,9 @@ cudaError_t launch_grad(const ScanArgs& a, int& parts, cudaStream_t st) {
   return a.packed ? grad_by<T, true>(a, parts, st) : grad_by<T, false>(a, parts, st);
 }
 
+// A CONV_ code.
 template <typename T>
-cudaError_t launch_step(const ScanStepArgs& a, cudaStream_t st) {
+int launch_step(const ScanStepArgs& a, cudaStream_t st) {
   constexpr int kV = 4;  // channels a thread: 8 bytes of a 16-bit type, 16 of fp32
   const int es = static_cast<int>(sizeof(T));
   const size_t v = static_cast<size_t>(es) * kV;
@@ -100,8 +101,10 @@ cudaError_t launch_step(const ScanStepArgs& a, cudaStream_t st) {
                    rows_aligned(a.i, 0, a.is, es, v) && aligned_to(a.y, v);
   const int per = kStepThreads * (vec ? kV : 1);
   const dim3 grid(a.B, (a.C + per - 1) / per);
-  return launch_pdl(vec ? gated_scan_step_kernel<T, kV> : gated_scan_step_kernel<T, 1>, grid, dim3(kStepThreads), 0,
-                    st, 1, a);
+  if (grid.y > 65535) return CONV_EUNSUPPORTED;
+  const cudaError_t e = launch_pdl(vec ? gated_scan_step_kernel<T, kV> : gated_scan_step_kernel<T, 1>, grid,
+                                   dim3(kStepThreads), 0, st, 1, a);
+  return e == cudaSuccess ? CONV_OK : CONV_ELAUNCH;
 }
 
 }  // namespace
@@ -267,10 +270,9 @@ int gated_scan_step(const void* x, const void* r, const void* i, const float* de
   if (any_alias(outs, 2, ins, 8)) return CONV_EALIAS;
   const ScanStepArgs a = {x, r, i, decay, h, index, y, B, slots, C, fill != 0, x_token, r_token, i_token, gate_consts()};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == CONV_F32   ? launch_step<float>(a, st)
-                        : dtype == CONV_F16 ? launch_step<__half>(a, st)
-                                            : launch_step<__nv_bfloat16>(a, st);
-  return e == cudaSuccess ? CONV_OK : CONV_ELAUNCH;
+  if (dtype == CONV_F32) return launch_step<float>(a, st);
+  if (dtype == CONV_F16) return launch_step<__half>(a, st);
+  return launch_step<__nv_bfloat16>(a, st);
 }
 
 }  // extern "C"

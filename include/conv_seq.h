@@ -15,9 +15,10 @@
  *    cu is read on the device and not checked; entries that decrease or lie
  *    outside [0, L] give unspecified results but no access out of bounds.
  * N, L and the step functions' B may be 0; C is at least 1; none is above
- * 2^31 - 4097.  A workspace is in use until the call's kernels are done:
- * calls that may overlap (other streams, graphs replayed side by side) need one
- * each.
+ * 2^31 - 4097.  The step functions take at most 65535 blocks of 128 channels, of
+ * 512 where C and the rows are aligned to four (CONV_EUNSUPPORTED).  A workspace
+ * is in use until the call's kernels are done: calls that may overlap (other
+ * streams, graphs replayed side by side) need one each.
  * Inputs documented with strides have unit channel stride, a token stride and
  * a batch stride in elements (batch stride unused when packed); every other
  * tensor is contiguous.  Buffers need only their element type's alignment;

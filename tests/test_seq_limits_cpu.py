@@ -86,3 +86,13 @@ def test_last_channels_and_sequences_are_refused(lib, T):
         for L, cu in ((0, None), (5, 1 << 55)):
             assert lib["conv_causal"](*T.conv_args(N=N, L=L, C=1, K=1, cu=cu, xb=0, xt=1, state=None, state_out=None, bias=None)) == T.EINVAL
             assert lib["gated_scan"](*T.scan_args(N=N, L=L, C=1, cu=cu, xb=0, rb=0, ib=0, h0=None, last=1 << 50, states=None)) == T.EINVAL
+
+
+def test_steps_refuse_channels_past_their_grid(lib, T):
+    """A step's channels lie along a grid dimension of 65535 blocks: more are refused before a launch that would fail."""
+    EUNSUPPORTED = -7
+    far = dict(y=1 << 50, w=1 << 51, state=1 << 52)
+    for C in (65535 * 128 + 1, 4 * 65535 * 128 + 4):
+        assert lib["conv_causal_step"](*T.conv_step_args(B=1, C=C, K=2, bias=None, xt=C, **far)) == EUNSUPPORTED
+        assert lib["gated_scan_step"](*T.scan_step_args(B=1, C=C, x=1 << 50, r=1 << 51, i=1 << 52, decay=1 << 53, h=1 << 54, y=1 << 55, xt=C,
+                                                        rt=C, it=C)) == EUNSUPPORTED
