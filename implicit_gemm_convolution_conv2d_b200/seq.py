@@ -57,6 +57,7 @@ def _lib():
         p, i, n = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
         size = [ctypes.c_ulonglong]
         out = [ctypes.POINTER(ctypes.c_ulonglong)]
+        table = {}
         for name, args in {
             "conv_causal": [p] * 7 + [i, n, i, i, n, n, i, i, i, p],
             "conv_causal_grad": [p] * 12 + [i, n, i, i] + [n] * 4 + [i, i, i, p] + size + [p],
@@ -71,7 +72,8 @@ def _lib():
         }.items():
             f = getattr(L, name)
             f.argtypes, f.restype = args, i
-            _fn[name] = f
+            table[name] = f
+        _fn.update(table)  # all at once: another thread may be looking
     return _fn
 
 

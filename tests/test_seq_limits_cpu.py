@@ -96,3 +96,30 @@ def test_steps_refuse_channels_past_their_grid(lib, T):
         assert lib["conv_causal_step"](*T.conv_step_args(B=1, C=C, K=2, bias=None, xt=C, **far)) == EUNSUPPORTED
         assert lib["gated_scan_step"](*T.scan_step_args(B=1, C=C, x=1 << 50, r=1 << 51, i=1 << 52, decay=1 << 53, h=1 << 54, y=1 << 55, xt=C,
                                                         rt=C, it=C)) == EUNSUPPORTED
+
+
+# ---- first use ----------------------------------------------------------
+
+
+def test_first_use_from_two_threads(monkeypatch):
+    """A thread that comes while another one looks the functions up finds all of them."""
+    import threading
+    import types
+
+    from implicit_gemm_convolution_conv2d_b200 import seq
+    found = {}
+
+    class Library:
+        def __getattr__(self, name):
+            if name == "gated_scan" and not found and threading.current_thread() is threading.main_thread():
+                found["..."] = None
+                other = threading.Thread(target=lambda: found.update(seq._lib()))
+                other.start()
+                other.join()
+            return types.SimpleNamespace()
+
+    library = Library()
+    monkeypatch.setattr(seq, "_load", lambda: library)
+    monkeypatch.setattr(seq, "_fn", {})
+    mine = seq._lib()
+    assert len(mine) == 10 and set(found) == set(mine) | {"..."}
