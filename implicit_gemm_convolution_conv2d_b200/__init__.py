@@ -241,16 +241,9 @@ def conv_wgrad(x, dy, kernel_size, stride=1, padding=0, dilation=1, groups=1, *,
     when `workspace` is None.
     """
     import torch
-    from .seq import Act8, act8_unpack
-    if isinstance(x, Act8):
-        if not (x.q.is_cuda and dy.is_cuda):
-            raise ValueError("conv_wgrad runs on CUDA tensors only")
-        if stream is not None:  # the temporary belongs to the stream that it is used on
-            with torch.cuda.stream(stream):
-                return conv_wgrad(x, dy, kernel_size, stride, padding, dilation, groups, padding_hi=padding_hi, out=out,
-                                  workspace=workspace)
-        return conv_wgrad(act8_unpack(x), dy, kernel_size, stride, padding, dilation, groups, padding_hi=padding_hi,
-                          out=out, workspace=workspace)
+    if not isinstance(x, torch.Tensor):
+        return _wgrad_of_checkpoint(x, dy, kernel_size, stride, padding, dilation, groups, padding_hi=padding_hi, out=out,
+                                    workspace=workspace, stream=stream)
     if not (x.is_cuda and dy.is_cuda):
         raise ValueError("conv_wgrad runs on CUDA tensors only")
     if x.dtype != dy.dtype:
@@ -293,6 +286,20 @@ def conv_wgrad(x, dy, kernel_size, stride=1, padding=0, dilation=1, groups=1, *,
     if rc:
         raise ConvError(rc, "conv_wgrad")
     return out
+
+
+def _wgrad_of_checkpoint(x, dy, *geometry, stream=None, **rest):
+    """conv_wgrad of an Act8 (the class is looked for here: calls with tensors do not load the sequence operators)."""
+    import torch
+    from .seq import Act8, act8_unpack
+    if not isinstance(x, Act8):
+        raise TypeError("conv_wgrad: x must be a tensor or an Act8")
+    if not (x.q.is_cuda and dy.is_cuda):
+        raise ValueError("conv_wgrad runs on CUDA tensors only")
+    if stream is not None:  # the temporary belongs to the stream that it is used on
+        with torch.cuda.stream(stream):
+            return conv_wgrad(act8_unpack(x), dy, *geometry, **rest)
+    return conv_wgrad(act8_unpack(x), dy, *geometry, **rest)
 
 
 def conv_wgrad_raw(x_ptr, dy_ptr, dw_ptr, geom, dtype, ws_ptr=None, ws_bytes=0, stream_handle=0):

@@ -123,3 +123,18 @@ def test_first_use_from_two_threads(monkeypatch):
     monkeypatch.setattr(seq, "_fn", {})
     mine = seq._lib()
     assert len(mine) == 10 and set(found) == set(mine) | {"..."}
+
+
+def test_convolutions_alone_load_no_sequence_operators():
+    """conv_wgrad of tensors looks for no checkpoint class."""
+    import os
+    import subprocess
+    import sys
+
+    code = ("import sys, torch, implicit_gemm_convolution_conv2d_b200 as cf\n"
+            "try:\n    cf.conv_wgrad(torch.zeros(1, 4, 4, 8), torch.zeros(1, 4, 4, 8), 3, padding=1)\n"
+            "except ValueError as e:\n    assert 'CUDA' in str(e)\n"
+            "assert cf.__name__ + '.seq' not in sys.modules\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
