@@ -235,7 +235,7 @@ def conv_wgrad(x, dy, kernel_size, stride=1, padding=0, dilation=1, groups=1, *,
     """Weight gradient of conv_fwd: dw[o, k, c] = sum over output pixels of dy * x.
 
     x: [N, (D,) H, W, C], or its 8-bit checkpoint (Act8), which is unpacked
-    into a temporary of dy's type; dy: [N, (Do,) Ho, Wo, O]; kernel_size: (kD,)
+    into a temporary of the type it had (that of dy too: another is refused); dy: [N, (Do,) Ho, Wo, O]; kernel_size: (kD,)
     kH, kW.  Returns dw [O, (kD,) kH, kW, C/groups] in x's dtype.  The call needs an
     fp32 workspace of wgrad_workspace_size bytes; one is allocated with torch
     when `workspace` is None.

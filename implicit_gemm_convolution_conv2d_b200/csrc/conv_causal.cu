@@ -51,7 +51,11 @@ int run_length(int N, long long L, int C, bool packed, int per_sm) {
   return run;
 }
 
-constexpr int kForwardPlaces = 3, kGradPlaces = 2;  // blocks an SM, by their registers
+// Blocks an SM of the K = 4 kernels, by their registers (76 to 80; gradients up to
+// 128).  Others are given the same count: with up to 3 taps (64 registers) four
+// forward blocks fit, with 5 to 8 (90 to 114) two, so that their grids leave a part
+// of a round.
+constexpr int kForwardPlaces = 3, kGradPlaces = 2;
 
 int grad_run(int N, long long L, int C, bool packed) { return run_length(N, L, C, packed, kGradPlaces); }
 
@@ -184,7 +188,7 @@ int conv_causal_grad(const void* x, const unsigned char* x_scale, const void* w,
   a.x = SeqIn{x, x_scale, x_batch, x_token}, a.dy = SeqIn{dy, nullptr, dy_batch, dy_token};
   a.w = w, a.bias = bias, a.state = state, a.cu = cu;
   a.dstate_out = window > 0 ? dstate_out : nullptr;
-  a.dx = dx, a.dw = dw, a.dbias = dbias, a.dstate = dstate, a.part = static_cast<float*>(workspace);
+  a.dx = dx, a.dstate = dstate, a.part = static_cast<float*>(workspace);
   a.N = N, a.C = C, a.K = K, a.silu = activation == CONV_ACT_SILU, a.fill = fill != 0;
   a.L = static_cast<int>(L);
   a.run = grad_run(N, L, C, packed);

@@ -29,7 +29,7 @@ struct CausalArgs {
   SeqIn x, dy;
   const void *w, *bias, *state, *dstate_out;
   const int* cu;
-  void *y, *state_out, *dx, *dw, *dbias, *dstate;
+  void *y, *state_out, *dx, *dstate;
   float* part;
   int N, C, K, silu, fill;
   int L;      // tokens of a sequence (packed: all rows)

@@ -23,9 +23,11 @@ int take_input(SeqIn& in, Span* s, const void* p, const unsigned char* scale, lo
   return CONV_OK;
 }
 
-// CTAs of a cluster, `tokens` each: enough that the grid has four CTAs for each
-// SM of a 148-SM B200 (a fixed number: the order of ddecay's sum must not depend
-// on the device), but no more than the tokens fill.
+// CTAs of a cluster, `tokens` each: the least power of two by which the grid has
+// four CTAs for each SM of a 148-SM B200 (a fixed number: the order of ddecay's sum
+// must not depend on the device), but no more than the tokens fill, nor eight.  Two
+// fit an SM (one of the f32 gradient's), so such a grid takes two rounds, the last
+// of them in part, and few channels of few sequences leave SMs without a CTA.
 int cluster_of(int N, long long L, int C, bool packed, int tokens) {
   const long long chains = (packed ? 1LL : N) * ((C + 63) / 64);
   const long long turns = (L + tokens - 1) / tokens;
@@ -222,7 +224,6 @@ int gated_scan_grad(const void* x, const unsigned char* x_scale, const void* r, 
   a.dx = dx;
   a.dr = dr;
   a.di = di;
-  a.ddecay = ddecay;
   a.dh0 = dh0;
   a.part = static_cast<float*>(workspace);
   a.N = N;

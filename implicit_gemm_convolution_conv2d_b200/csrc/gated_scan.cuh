@@ -167,7 +167,7 @@ struct ScanArgs {
   const float *decay, *h0, *dh_last;
   const int* cu;
   void *y, *dx, *dr, *di;
-  float *h_last, *states, *ddecay, *dh0, *part;
+  float *h_last, *states, *dh0, *part;
   const float* states_in;
   int N, C, packed, fill;
   long long L;
@@ -176,9 +176,10 @@ struct ScanArgs {
 
 // ---- one pass over time --------------------------------------------------
 //
-// A warp owns 64 neighbouring channels, two a lane, and a few tokens in a row; a CTA is kScanWarps warps, one behind the other in time; a cluster
-// is up to eight CTAs one behind the other, and walks along a sequence in turns
-// of as many tokens as it holds.  A segment of tokens is the map
+// A warp owns 64 neighbouring channels, two a lane, and a few tokens in a row; a
+// CTA is kScanWarps warps, one behind the other in time; a cluster is up to eight
+// CTAs one behind the other, and walks along a sequence in turns of as many tokens
+// as it holds.  A segment of tokens is the map
 // h -> P h + H (P the product of its a's, H its own end state), so per turn the
 // warps leave (P, H) in shared memory, the CTAs' maps go to every CTA of the
 // cluster through distributed shared memory, and once they are there every

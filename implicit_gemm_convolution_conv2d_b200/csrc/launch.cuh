@@ -1,12 +1,13 @@
 // launch.cuh -- host-side kernel launch with programmatic stream serialization.
 //
-// Every kernel of this library lets the next launch on its stream start once
-// its own setup (barrier init, tensor-memory allocation, tensor-map prefetch)
-// is done, and waits for the previous grid on the stream to complete, with its
-// writes visible, before its first access to global memory (ptx::pdl_* at the
-// end of each kernel's setup).  Launched with the attribute below, a kernel's
-// launch and setup then overlap the last CTAs of the kernel before it; the
-// results are those of plain stream order.
+// Every kernel of this library waits for the previous grid on the stream to
+// complete, with its writes visible, before its first access to global memory
+// (ptx::pdl_wait_prev).  The convolution kernels that have a setup (barrier init,
+// tensor-memory allocation, tensor-map prefetch) also let the next launch start
+// once it is done (ptx::pdl_allow_next); behind the others, the weight gradient's
+// and the sequence operators' among them, it starts as their CTAs exit.  Launched
+// with the attribute below, a kernel's launch and setup then overlap the last CTAs
+// of the kernel before it; the results are those of plain stream order.
 #pragma once
 
 #include <cuda_runtime.h>

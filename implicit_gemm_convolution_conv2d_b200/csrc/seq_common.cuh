@@ -195,7 +195,9 @@ __device__ __forceinline__ int seq_of_row(const int* __restrict__ cu, int n, lon
 }
 
 // Whether requests before and after row b name the same slot: bit 0 an earlier
-// one, bit 1 a later one.  Called by whole warps; the answer is warp-uniform.
+// one, bit 1 a later one.  Called by whole warps; the answer is warp-uniform.  Each
+// warp reads the whole index: nothing beside a launch at some hundred requests, the
+// larger part of a step at tens of thousands.
 __device__ __forceinline__ int same_slot(const int* __restrict__ index, int B, int b, int slot) {
   bool earlier = false, later = false;
   for (int k = threadIdx.x & 31; k < B; k += 32) {
@@ -286,7 +288,7 @@ inline bool rows_aligned(const void* p, long long batch, long long token, int es
          (token * esize) % static_cast<long long>(a) == 0;
 }
 
-// CTAs that fill the device once with `per_sm` blocks an SM.
+// SMs of the current device.
 inline int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||

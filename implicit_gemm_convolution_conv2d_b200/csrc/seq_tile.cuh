@@ -109,7 +109,6 @@ __device__ __forceinline__ void expand8(RowTile<T, STEPS>& tile, int first, int 
   __syncwarp();
 }
 
-
 // Moves the bytes of rows 8 k .. 8 k + 7, which lie behind those of the rows in
 // front of them, to the beginning of the tile's row 8 k.  Whole warps; the last
 // eight first.

@@ -211,8 +211,9 @@ def _saved(v, what, name):
 def act8_pack(x, *, stream=None) -> Act8:
     """x [..., C] in 8 bits: blocks of 32 channels share a power of two, the
     least by which the block's largest magnitude is at most 127, and each element
-    is rounded to the nearest multiple of it (off by at most half of it).  A
-    block with an infinity or NaN comes back as NaN."""
+    is rounded to the nearest multiple of it: off by at most half of it, or by less
+    than one where that multiple would be past the type's largest value (65504 in
+    float16 comes back as 64512).  A block with an infinity or NaN comes back as NaN."""
     what = "act8_pack"
     _cuda(x, "x", what)
     code = _code(x.dtype, what)
@@ -450,7 +451,8 @@ def gated_scan_grad(x, r, i, decay, dy, states, *, h0=None, dh_last=None, cu_seq
     y, and `dh_last`, that of the last states (if it matters).
 
     x, r and i may each be the activation or its checkpoint (Act8; a mixture is
-    unpacked into temporaries); `states` are the forward pass's.  ddecay and dh0 are fp32; dh0 is None without h0."""
+    unpacked into temporaries); `states` are the forward pass's.  ddecay and dh0 are
+    fp32; dh0 is None without h0."""
     what = "gated_scan_grad"
     xv, xs, dtype = _saved(x, what, "x")
     rv, rs, rd = _saved(r, what, "r")

@@ -63,7 +63,9 @@ int conv_causal(const void* x, const void* w, const void* bias, const void* stat
  * dstate_out (may be NULL) is the gradient of the forward pass's state_out.
  * dw and dbias are sums over all tokens: fp32 partial sums of fixed ranges of
  * tokens in `workspace` (conv_causal_grad_workspace_size bytes, 16-byte
- * aligned), added in order, so a result is the same bits on every run. */
+ * aligned), added in order, so a result is the same bits on every run.  Eight
+ * ranges take K + 1 rows of C there, and in a batch each sequence has ranges of its
+ * own: many sequences of a few tokens take less packed. */
 int conv_causal_grad(const void* x, const unsigned char* x_scale, const void* w, const void* bias, const void* state,
                      const int* cu, const void* dy, const void* dstate_out, void* dx, void* dw, void* dbias,
                      void* dstate, int N, long long L, int C, int K, long long x_batch, long long x_token,
@@ -93,7 +95,7 @@ int conv_causal_step(const void* x, const void* w, const void* bias, void* state
  * receives the state in front of every GATED_SCAN_STATE_EVERY-th token,
  * [N, ceil(L/64), C] (packed: of every 64th row, [ceil(L/64), C]): the backward
  * pass starts from them.  Entries in front of a sequence's first token, or of
- * unused rows, are finite but have no meaning. */
+ * unused rows, are written but have no meaning. */
 #define GATED_SCAN_STATE_EVERY 64
 
 int gated_scan(const void* x, const void* r, const void* i, const float* decay, const float* h0, const int* cu, void* y,
@@ -107,7 +109,8 @@ int gated_scan(const void* x, const void* r, const void* i, const float* decay, 
  * [C] and dh0 [N, C] (fp32; dh0 may be NULL).  dh_last (fp32, may be NULL) is
  * the gradient of h_last.  Where 1 - a^2 is below fp32's least normal number
  * (decay * s under 6e-39, or 0) it counts as 0, as in the forward pass, and the
- * square root's derivative is taken as 0.  ddecay is summed as dw above is. */
+ * square root's derivative is taken as 0.  ddecay is summed as dw above is, from a
+ * row of C partial sums of each CTA: one at least of each sequence of a batch. */
 int gated_scan_grad(const void* x, const unsigned char* x_scale, const void* r, const unsigned char* r_scale,
                     const void* i, const unsigned char* i_scale, const float* decay, const float* states,
                     const float* h0, const int* cu, const void* dy, const float* dh_last, void* dx, void* dr, void* di,
@@ -130,7 +133,8 @@ int gated_scan_step(const void* x, const void* r, const void* i, const float* de
  * one power of two 2^e, the least with |x| <= 127 * 2^e for all its elements
  * and e >= -126, and its elements are q = x / 2^e rounded to the nearest
  * integer (ties to even), held within the type's largest value: x is given
- * back as q * 2^e, off by at most 2^(e-1).  scale holds e + 127; 0 for a block
+ * back as q * 2^e, off by at most 2^(e-1), or by less than 2^e where the nearest
+ * is past that value (65504 in f16 is 63 * 2^10).  scale holds e + 127; 0 for a block
  * of zeros; 255 for a block with an infinity or NaN, whose elements all come
  * back as NaN (q = 0 there).
  * x: [rows, C] with a row stride; q: [rows, C] int8; scale: [rows, ceil(C/32)]
