@@ -42,19 +42,21 @@ __device__ __forceinline__ Vf<V> both(const float2& c) {
   return o;
 }
 
-// The sigmoids of the forward pass share a reciprocal: the special functions, 16 a
-// clock and SM, are its first limit, and this leaves 5 of them an element (with 6,
-// 65536 x 2048 bf16 takes 381 us in place of 367).  With E_r = 1 + e^-r and E_i =
-// 2^-124 (1 + e^-i) the product E_r E_i is a normal number unless both gates are
-// below 2^-124 (where both then are 0), so s = E_i / (E_r E_i) and g = 2^-124 E_r /
-// (E_r E_i) are right down to fp32's least normal number, at r or i = -87.3.
-// Below, at -infinity too, they are 0: r and i stop at -87.5, and the last product
-// takes what is subnormal as 0.  A NaN in either gate makes both NaN, as it makes
-// u = m g x and every state behind it.
+// In the forward pass of 16-bit types the two sigmoids share a reciprocal: the
+// special functions, 16 a clock and SM, are its first limit, and this leaves 5 of
+// them an element (with 6, 65536 x 2048 bf16 takes 381 us in place of 359).  With
+// E_r = 1 + e^-r and E_i = 2^-124 (1 + e^-i) the product E_r E_i is a normal number
+// unless both gates are below 2^-124 (where both then are 0), so s = E_i / (E_r E_i)
+// and g = 2^-124 E_r / (E_r E_i) are right down to fp32's least normal number, at r
+// or i = -87.3.  Below, at -infinity too, they are 0: r and i stop at -87.5, and the
+// last product takes what is subnormal as 0.  A NaN in either gate makes both NaN,
+// as it makes u = m g x and every state behind it.
 //
-// In the backward pass that would be wrong, as a NaN in i leaves a, and through it
-// the gradients of earlier tokens, as they are: there each sigmoid has a reciprocal
-// of its own, whose flush of subnormal results closes the gates at the same place.
+// Elsewhere each has a reciprocal of its own, whose flush of subnormal results
+// closes the gates at the same place: in the backward pass, where a NaN in i leaves
+// a, and through it the gradients of earlier tokens, as they are; for fp32, whose
+// bytes take longer than six special functions (4 x 4096 x 2560: 133 us, with a
+// shared one 136); and for single tokens, which wait for the memory.
 constexpr float kGateLowest = -87.5f;  // exact in each type; e^87.5 is finite
 
 // a b, with subnormal results as 0
@@ -80,9 +82,9 @@ struct GateValues {
   Vf<V> s, g, a, m;
 };
 
-// FORWARD: a shared reciprocal, r and i at least kGateLowest, and m = sqrt(1 - a^2);
-// else a reciprocal each, any r and i, and 1 - a^2 in m.
-template <int V, bool FORWARD = true>
+// SHARED: one reciprocal, r and i at least kGateLowest.  ROOT: m = sqrt(1 - a^2),
+// else 1 - a^2.
+template <int V, bool SHARED, bool ROOT>
 __device__ __forceinline__ GateValues<V> gate_values(const GateConsts& c, const Vf<V>& r, const Vf<V>& i,
                                                      const Vf<V>& decay) {
   GateValues<V> o;
@@ -91,7 +93,7 @@ __device__ __forceinline__ GateValues<V> gate_values(const GateConsts& c, const 
 #pragma unroll
   for (int k = 0; k < V; ++k) er[k] = ex2_approx(er[k]), ei[k] = ex2_approx(ei[k]);
   er = add_v(er, one);
-  if constexpr (FORWARD) {
+  if constexpr (SHARED) {
     const Vf<V> unit = both<V>(c.unit);
     ei = fma_v(ei, unit, unit);
     Vf<V> inv = mul_v(er, ei);
@@ -123,7 +125,7 @@ __device__ __forceinline__ GateValues<V> gate_values(const GateConsts& c, const 
     o.a[k] = near1 ? near_a[k] : far[k];
   }
   o.m = mul_v(E, fma_v(E, none, both<V>(c.two)));
-  if constexpr (FORWARD) {
+  if constexpr (ROOT) {
 #pragma unroll
     for (int k = 0; k < V; ++k) o.m[k] = sqrt_approx(o.m[k]);
   }
@@ -134,31 +136,19 @@ __device__ __forceinline__ Vf<V> gated_input(const GateValues<V>& v, const Vf<V>
   return mul_v(mul_v(m, v.g), x);
 }
 
-template <int V>
-__device__ __forceinline__ Vf<V> lowest(Vf<V> v) {
-#pragma unroll
-  for (int k = 0; k < V; ++k) v[k] = max_nan(v[k], kGateLowest);
-  return v;
-}
-// Gates as they are in memory, at least kGateLowest (NaN stays).
-template <typename T, int V>
-__device__ __forceinline__ Vf<V> gate_input(Raw<T, V> raw) {
-  Vf<V> o;
-  if constexpr (sizeof(T) == 2 && V == 2) {
-    const float2 lowest = make_float2(kGateLowest, kGateLowest);
-    uint32_t w = raw;
-    if constexpr (std::is_same<T, __half>::value) {
-      const __half2 l = __float22half2_rn(lowest);
-      asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(w) : "r"(*reinterpret_cast<const uint32_t*>(&l)));
-    } else {
-      const __nv_bfloat162 l = __float22bfloat162_rn(lowest);
-      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(*reinterpret_cast<const uint32_t*>(&l)));
-    }
-    unpack<T, V>(w, o.v);
+// Two gates of a 16-bit type as they are in memory, at least kGateLowest (NaN stays).
+template <typename T>
+__device__ __forceinline__ Vf<2> gate_input(uint32_t w) {
+  const float2 lowest = make_float2(kGateLowest, kGateLowest);
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 l = __float22half2_rn(lowest);
+    asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(w) : "r"(*reinterpret_cast<const uint32_t*>(&l)));
   } else {
-    unpack<T, V>(raw, o.v);
-    o = lowest(o);
+    const __nv_bfloat162 l = __float22bfloat162_rn(lowest);
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(*reinterpret_cast<const uint32_t*>(&l)));
   }
+  Vf<2> o;
+  unpack<T, 2>(w, o.v);
   return o;
 }
 
@@ -463,10 +453,16 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const __gri
       constexpr bool EDGE = decltype(e)::value;
 #pragma unroll
       for (int j = 0; j < STEPS; ++j) {
-        const GateValues<V> g = gate_values<V>(a.consts, gate_input<T, V>(row_pair(tile.r, j, lane)),
-                                               gate_input<T, V>(row_pair(tile.i, j, lane)), decay);
-        Vf<V> xv;
+        constexpr bool SHARED = sizeof(T) == 2;
+        Vf<V> rv, iv, xv;
+        if constexpr (SHARED) {
+          rv = gate_input<T>(row_pair(tile.r, j, lane)), iv = gate_input<T>(row_pair(tile.i, j, lane));
+        } else {
+          unpack<T, V>(row_pair(tile.r, j, lane), rv.v);
+          unpack<T, V>(row_pair(tile.i, j, lane), iv.v);
+        }
         unpack<T, V>(row_pair(tile.x, j, lane), xv.v);
+        const GateValues<V> g = gate_values<V, SHARED, true>(a.consts, rv, iv, decay);
         u[j] = gated_input<V>(g, g.m, xv);
         av[j] = g.a;
         if (EDGE && (tok.first >> j & 1))
@@ -668,7 +664,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_grad_kernel(const 
     ScanMap<V> fwd = no_map<V>(), bwd = no_map<V>();
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
-      const GateValues<V> gv = gate_values<V, false>(a.consts, row_of(tile.r, j), row_of(tile.i, j), decay);
+      const GateValues<V> gv = gate_values<V, false, false>(a.consts, row_of(tile.r, j), row_of(tile.i, j), decay);
 #pragma unroll
       for (int k = 0; k < V; ++k) over[j][k] = gv.m[k] >= kLeastNormal ? rsqrt_approx(gv.m[k]) : gv.m[k];
       mv[j] = mul_v(gv.m, over[j]);
@@ -813,7 +809,7 @@ __global__ void __launch_bounds__(kStepThreads) gated_scan_step_kernel(const Sca
     unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.x) + b * a.xs + c), x.v);
     unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.r) + b * a.rs + c), r.v);
     unpack<T, V>(load_raw<T, V>(static_cast<const T*>(a.i) + b * a.is + c), i.v);
-    const GateValues<V> v = gate_values<V>(a.consts, lowest(r), lowest(i), decay);
+    const GateValues<V> v = gate_values<V, false, true>(a.consts, r, i, decay);
     h = fma_v(v.a, h, gated_input<V>(v, v.m, x));
     store_vec<T, V>(y + static_cast<long long>(b) * a.C, h.v);
     if (!(others & 2)) break;
