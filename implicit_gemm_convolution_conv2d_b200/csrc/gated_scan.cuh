@@ -387,10 +387,10 @@ __device__ __forceinline__ Vf<V> scan_exchange(ScanShared<V>& sh, int b, int ord
 
 // The forward pass.  Bounds: 8 bytes an element of a 16-bit type, and five
 // special functions (40 of an SM quarter's cycles for 32 elements, where the
-// bytes take 44).  Measured: 65536 x 2048 bf16 in 360 us, 2.98 TB/s (46 % of the
-// copy rate), 4 x 4096 x 2560 bf16 in 105 us, fp32 in 132 (5.1 TB/s); without
+// bytes take 44).  Measured: 65536 x 2048 bf16 in 359 us, 2.99 TB/s (46 % of the
+// copy rate), 4 x 4096 x 2560 bf16 in 108 us, fp32 in 133 (5.0 TB/s); without
 // its loads or its stores it takes as long, so what bounds it is the issue of
-// some 42 instructions an element at 16 warps an SM and the exchange of a turn.
+// some 41 instructions an element at 16 warps an SM and the exchange of a turn.
 // Tokens of a warp: the maps of a turn cost as much however many there are, but
 // a and u of each stay in registers.  16 tokens and 2 CTAs an SM: 364 us; 8
 // tokens and 3 or 4 CTAs: 420, 524; 4 or 16 warps a CTA: 416, 539; computing the
@@ -515,10 +515,10 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const __gri
 // ---- the backward pass -----------------------------------------------------
 //
 // Bounds: 14 bytes an element of a 16-bit type (11.1 from checkpoints).  Measured:
-// 4 x 4096 x 2560 bf16 in 217 us, 2.7 TB/s (41 % of the copy rate), from
-// checkpoints 237; fp32 333 (3.5 TB/s); 16000 rows x 2048 f16 in 29 sequences from
-// checkpoints 250.  It issues some 90 instructions an element at 52 % of the
-// rate, at 16 warps an SM; keeping s and m in shared memory instead of in spilled
+// 4 x 4096 x 2560 bf16 in 207 us, 2.8 TB/s (43 % of the copy rate), from
+// checkpoints 229; fp32 340 (3.45 TB/s; its shared memory holds one CTA an SM);
+// 16000 rows x 2048 f16 in 29 sequences from checkpoints 252.  It issues some 86
+// instructions an element at 50 % of the rate, at 16 warps an SM; keeping s and m in shared memory instead of in spilled
 // registers took 232 -> 217, expanding checkpoints to tiles once instead of at
 // each use 574 -> 237.
 
