@@ -60,16 +60,11 @@ __device__ __forceinline__ Vf<V> both(const float2& c) {
 constexpr float kGateLowest = -87.5f;  // exact in each type; e^87.5 is finite
 
 // a b, with subnormal results as 0
-template <int V>
-__device__ __forceinline__ Vf<V> mul_ftz(const Vf<V>& a, const Vf<V>& b) {
-  Vf<V> o;
-#pragma unroll
-  for (int k = 0; k + 1 < V; k += 2) {
-    uint64_t d;
-    asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pack2(a.v + k)), "l"(pack2(b.v + k)));
-    unpack2(d, o.v + k);
-  }
-  if constexpr (V & 1) asm("mul.rn.ftz.f32 %0, %1, %2;" : "=f"(o[V - 1]) : "f"(a[V - 1]), "f"(b[V - 1]));
+__device__ __forceinline__ Vf<2> mul_ftz(const Vf<2>& a, const Vf<2>& b) {
+  uint64_t d;
+  asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pack2(a.v)), "l"(pack2(b.v)));
+  Vf<2> o;
+  unpack2(d, o.v);
   return o;
 }
 
@@ -82,7 +77,7 @@ struct GateValues {
   Vf<V> s, g, a, m;
 };
 
-// SHARED: one reciprocal, r and i at least kGateLowest.  ROOT: m = sqrt(1 - a^2),
+// SHARED (V = 2): one reciprocal, r and i at least kGateLowest.  ROOT: m = sqrt(1 - a^2),
 // else 1 - a^2.
 template <int V, bool SHARED, bool ROOT>
 __device__ __forceinline__ GateValues<V> gate_values(const GateConsts& c, const Vf<V>& r, const Vf<V>& i,
@@ -518,8 +513,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) gated_scan_kernel(const __gri
 // 4 x 4096 x 2560 bf16 in 207 us, 2.8 TB/s (43 % of the copy rate), from
 // checkpoints 229; fp32 340 (3.45 TB/s; its shared memory holds one CTA an SM);
 // 16000 rows x 2048 f16 in 29 sequences from checkpoints 252.  It issues some 86
-// instructions an element at 50 % of the rate, at 16 warps an SM; keeping s and m in shared memory instead of in spilled
-// registers took 232 -> 217, expanding checkpoints to tiles once instead of at
+// instructions an element at 50 % of the rate, at 16 warps an SM; keeping s and m
+// in shared memory instead of in spilled registers took 232 -> 217, a reciprocal
+// for each sigmoid 214 -> 207, expanding checkpoints to tiles once instead of at
 // each use 574 -> 237.
 
 // x, r and i of the backward pass on their way to the tiles: elements with

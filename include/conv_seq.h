@@ -89,13 +89,13 @@ int conv_causal_step(const void* x, const void* w, const void* bias, void* state
  *
  * for each channel within each sequence, from h0 [N, C] (fp32; zero if NULL).
  * decay: [C] fp32, >= 0; an infinite one counts as fp32's largest number.  A
- * sigmoid below fp32's least normal number (a gate under -87.3) is 0.  The state and all sums are fp32; y is h rounded to
- * the type of x, r and i.  h_last [N, C] (fp32, may be NULL) receives each
- * sequence's last state (h0 for an empty one).  states (fp32, may be NULL)
- * receives the state in front of every GATED_SCAN_STATE_EVERY-th token,
- * [N, ceil(L/64), C] (packed: of every 64th row, [ceil(L/64), C]): the backward
- * pass starts from them.  Entries in front of a sequence's first token, or of
- * unused rows, are written but have no meaning. */
+ * sigmoid below fp32's least normal number (a gate under -87.3) is 0.  The state
+ * and all sums are fp32; y is h rounded to the type of x, r and i.  h_last [N, C]
+ * (fp32, may be NULL) receives each sequence's last state (h0 for an empty one).
+ * states (fp32, may be NULL) receives the state in front of every
+ * GATED_SCAN_STATE_EVERY-th token, [N, ceil(L/64), C] (packed: of every 64th row,
+ * [ceil(L/64), C]): the backward pass starts from them.  Entries in front of a
+ * sequence's first token, or of unused rows, are written but have no meaning. */
 #define GATED_SCAN_STATE_EVERY 64
 
 int gated_scan(const void* x, const void* r, const void* i, const float* decay, const float* h0, const int* cu, void* y,
